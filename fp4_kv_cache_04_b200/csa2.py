@@ -38,6 +38,10 @@ CACHE_OFF, CACHE_FILL, CACHE_USE = 0, 1, 2
 SWA_BF16, SWA_FP8 = 0, 1
 Q_BF16, Q_NVFP4 = 0, 1
 
+T_BF16, T_F16, T_F32 = 0, 1, 2
+ROPE_NORM, ROPE_INVERSE, ROPE_HALF = 1, 2, 4
+TYPES = {torch.bfloat16: T_BF16, torch.float16: T_F16, torch.float32: T_F32}
+
 OK = 0
 STATUS_NAMES = {0: "CSA2_OK", 1: "CSA2_ERR_INVALID_ARG", 2: "CSA2_ERR_UNSUPPORTED",
                 3: "CSA2_ERR_WORKSPACE", 4: "CSA2_ERR_CUDA", 5: "CSA2_ERR_TIMEOUT",
@@ -47,7 +51,9 @@ EXPORTED = ["csa2_status_string", "csa2_last_error", "csa2_abi_version",
             "csa2_kernel_launches", "csa2_quantize_kv", "csa2_append_kv",
             "csa2_index_score", "csa2_topk", "csa2_pool_workspace_size", "csa2_build_pool",
             "csa2_build_pool_noalloc",
-            "csa2_workspace_size", "csa2_attend", "csa2_check_device_status", "csa2_set_wait_limit"]
+            "csa2_workspace_size", "csa2_attend", "csa2_check_device_status", "csa2_set_wait_limit",
+            "csa2_norm_rope", "csa2_append_rope", "csa2_dequantize_kv", "csa2_cache_workspace_size",
+            "csa2_attend_cache"]
 
 
 class Csa2Error(RuntimeError):
@@ -90,6 +96,39 @@ class LayerArgs(ctypes.Structure):
                 ("reserved2", ctypes.c_int32), ("ev_pool", ctypes.c_void_p)]
 
 
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("in_type", ctypes.c_int32), ("out_type", ctypes.c_int32),
+                ("flags", ctypes.c_int32), ("x_row_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64), ("x", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("eps", ctypes.c_float), ("reserved0", ctypes.c_int32)]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("batch", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+                ("idx_rope_dim", ctypes.c_int32), ("in_type", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("latent_stride", ctypes.c_int64), ("idx_stride", ctypes.c_int64),
+                ("total_rows", ctypes.c_int64), ("latent", ctypes.c_void_p), ("idx_proj", ctypes.c_void_p),
+                ("seq", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("kv_offsets", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("page_rows", ctypes.c_int32),
+                ("pages_per_seq", ctypes.c_int32), ("inv_freq", ctypes.c_void_p),
+                ("idx_inv_freq", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("idx_k", ctypes.c_void_p), ("idx_kscale", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p)]
+
+
+class CacheArgs(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("q_per_seq", ctypes.c_int32), ("ratio", ctypes.c_int32),
+                ("out_type", ctypes.c_int32), ("max_n", ctypes.c_int64), ("total_n", ctypes.c_int64),
+                ("window", ctypes.c_int64), ("sinks", ctypes.c_int64), ("kv_offsets", ctypes.c_void_p),
+                ("q_pos", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("sm_scale", ctypes.c_float), ("reserved0", ctypes.c_int32),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("page_rows", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _lib.csa2_status_string.restype = ctypes.c_char_p
 _lib.csa2_status_string.argtypes = [_i32]
@@ -114,6 +153,16 @@ _lib.csa2_workspace_size.restype = _sz
 _lib.csa2_workspace_size.argtypes = [ctypes.POINTER(LayerArgs)]
 _lib.csa2_attend.restype = _i32
 _lib.csa2_attend.argtypes = [ctypes.POINTER(LayerArgs), _vp]
+_lib.csa2_norm_rope.restype = _i32
+_lib.csa2_norm_rope.argtypes = [ctypes.POINTER(RopeArgs), _vp]
+_lib.csa2_append_rope.restype = _i32
+_lib.csa2_append_rope.argtypes = [ctypes.POINTER(AppendArgs), _vp]
+_lib.csa2_dequantize_kv.restype = _i32
+_lib.csa2_dequantize_kv.argtypes = [_vp, _vp, _i64, _vp, _i64, _vp, _vp]
+_lib.csa2_cache_workspace_size.restype = _sz
+_lib.csa2_cache_workspace_size.argtypes = [ctypes.POINTER(CacheArgs)]
+_lib.csa2_attend_cache.restype = _i32
+_lib.csa2_attend_cache.argtypes = [ctypes.POINTER(CacheArgs), _vp]
 _lib.csa2_check_device_status.restype = _i32
 _lib.csa2_check_device_status.argtypes = [_vp, _vp]
 _lib.csa2_set_wait_limit.restype = _i32
@@ -283,3 +332,170 @@ def set_wait_limit(workspace: torch.Tensor, polls: int, stream=None) -> None:
     """Bound (in polls) of the device-side waits of later calls with this workspace; 0 =
     the library default."""
     _check(_lib.csa2_set_wait_limit(_ptr(workspace), int(polls), _stream(stream)), "csa2_set_wait_limit")
+
+
+# ------------------------------------------------------------------ dense use of the cache
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(f"libcsa2: {what}")
+
+
+def _same_device(args, *tensors) -> None:
+    """The tensors' device goes with the argument block: a call from another current device
+    would launch there on this one's pointers."""
+    devs = {t.device for t in tensors if t is not None}
+    _need(len(devs) == 1, f"tensors on different devices: {sorted(map(str, devs))}")
+    args.device = devs.pop().index
+    args.tensors = tensors                     # alive as long as the block that points at them
+
+
+def _on_device(args, where: str) -> None:
+    _need(torch.cuda.current_device() == args.device,
+          f"{where}: the tensors are on cuda:{args.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _vec(t: torch.Tensor | None, dtype, n: int, what: str) -> int | None:
+    if t is None:
+        return None
+    _need(t.dtype == dtype and t.numel() == n, f"{what}: {n} values of {dtype} expected, got {t.numel()} of {t.dtype}")
+    return _ptr(t)
+
+
+def _strided(t: torch.Tensor, what: str) -> int:
+    """Device pointer of a tensor whose last dimension is contiguous."""
+    if not t.is_cuda:
+        raise ValueError("libcsa2 takes CUDA tensors")
+    _need(t.dtype in TYPES, f"{what}: bf16, f16 or fp32 expected, got {t.dtype}")
+    _need(t.shape[-1] <= 1 or t.stride(-1) == 1, f"{what}: the last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _step(t: torch.Tensor, dim: int) -> int:
+    """Stride of a dimension; 0 where it has one element, whatever torch says there."""
+    return t.stride(dim) if t.shape[dim] > 1 else 0
+
+
+def rope_args(*, x: torch.Tensor, out: torch.Tensor, pos: torch.Tensor | None = None,
+              inv_freq: torch.Tensor | None = None, weight: torch.Tensor | None = None, norm: bool = True,
+              eps: float = 1e-6, inverse: bool = False, half: bool = False) -> RopeArgs:
+    """Arguments of norm_rope.  x, out: [rows][heads][dim] (any row and head strides, last
+    dimension contiguous; bf16 / f16 / fp32 each); out may be x.  pos int64 [rows] and
+    inv_freq fp32 [r/2] rotate the last r channels of each vector (both None: no rotation);
+    weight fp32 [dim] or None with norm.  inverse turns back, half pairs (i, i + r/2)."""
+    _need(x.dim() == 3 and out.shape == x.shape, "x and out are [rows][heads][dim] of one shape")
+    rows, heads, dim = x.shape
+    _need((pos is None) == (inv_freq is None), "pos and inv_freq go together")
+    r = 0 if inv_freq is None else 2 * inv_freq.numel()
+    flags = (ROPE_NORM if norm else 0) | (ROPE_INVERSE if inverse else 0) | (ROPE_HALF if half else 0)
+    a = RopeArgs(rows, heads, dim, r, TYPES.get(x.dtype, -1), TYPES.get(out.dtype, -1), flags, _step(x, 0), _step(x, 1),
+                 _step(out, 0), _step(out, 1), _strided(x, "x"), _strided(out, "out"),
+                 _vec(pos, torch.int64, rows, "pos"), _vec(inv_freq, torch.float32, r // 2, "inv_freq"),
+                 _vec(weight, torch.float32, dim, "weight"), eps, 0)
+    _same_device(a, x, out, pos, inv_freq, weight)
+    return a
+
+
+def norm_rope(args: RopeArgs, stream=None) -> None:
+    """Head norm and rotary positions in one pass (csa2_norm_rope)."""
+    _on_device(args, "norm_rope")
+    _check(_lib.csa2_norm_rope(ctypes.byref(args), _stream(stream)), "csa2_norm_rope")
+
+
+def append_args(*, latent: torch.Tensor, pos: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                seq: torch.Tensor | None = None, kv_offsets: torch.Tensor | None = None,
+                page_table: torch.Tensor | None = None, page_rows: int = 0, weight: torch.Tensor | None = None,
+                norm: bool = True, eps: float = 1e-6, inv_freq: torch.Tensor | None = None, half: bool = False,
+                idx_proj: torch.Tensor | None = None, idx_inv_freq: torch.Tensor | None = None,
+                idx_k: torch.Tensor | None = None, idx_kscale: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None) -> AppendArgs:
+    """Arguments of append_rope.  latent [n][512] (bf16 / f16 / fp32, any row stride), pos
+    int64 [n] (-1: padding), seq int32 [n] or None (token i belongs to sequence i); the cache
+    packed by kv_offsets or paged; idx_proj fp32 [n][64] with idx_k / idx_kscale adds the
+    indexer rows."""
+    n = latent.shape[0]
+    _need(latent.dim() == 2 and latent.shape[1] == D, "latent is [n][512]")
+    _need(codes.dtype == torch.uint8 and scales.dtype == torch.uint8 and codes.dim() == 2 and scales.dim() == 2 and
+          codes.shape[1] == ROW_CODES and scales.shape[1] == ROW_SCALES and codes.shape[0] == scales.shape[0],
+          "codes uint8 [rows][256] and scales uint8 [rows][32]")
+    total = codes.shape[0]
+    _need((kv_offsets is None) != (page_table is None), "either kv_offsets or page_table")
+    if page_table is not None:
+        _need(page_table.dtype == torch.int32 and page_table.dim() == 2, "page_table is int32 [batch][pages]")
+        batch, pages = page_table.shape
+    else:
+        _need(kv_offsets.dtype == torch.int64 and kv_offsets.numel() >= 2, "kv_offsets is int64 [batch+1]")
+        batch, pages = kv_offsets.numel() - 1, 0
+    if idx_proj is not None:
+        _need(idx_proj.dtype == torch.float32 and tuple(idx_proj.shape) == (n, IDX_DIM), "idx_proj is fp32 [n][64]")
+        _need(idx_k is not None and idx_kscale is not None and idx_k.dtype == torch.uint8 and
+              tuple(idx_k.shape) == (total, IDX_DIM), "idx_k uint8 [rows][64] and idx_kscale fp32 [rows] with idx_proj")
+    r = 0 if inv_freq is None else 2 * inv_freq.numel()
+    ri = 0 if idx_inv_freq is None else 2 * idx_inv_freq.numel()
+    _need(workspace is None or workspace.numel() >= 256, "workspace of 256 bytes or more")
+    a = AppendArgs(n, batch, r, ri, TYPES.get(latent.dtype, -1), (ROPE_NORM if norm else 0) | (ROPE_HALF if half else 0),
+                   eps, _step(latent, 0) if n > 1 else D, 0 if idx_proj is None else _step(idx_proj, 0) if n > 1 else IDX_DIM, total,
+                   _strided(latent, "latent"), None if idx_proj is None else _strided(idx_proj, "idx_proj"),
+                   _vec(seq, torch.int32, n, "seq"), _vec(pos, torch.int64, n, "pos"), _ptr(kv_offsets), _ptr(page_table),
+                   int(page_rows) if page_table is not None else 0, pages, _vec(inv_freq, torch.float32, r // 2, "inv_freq"),
+                   _vec(idx_inv_freq, torch.float32, ri // 2, "idx_inv_freq"), _vec(weight, torch.float32, D, "weight"),
+                   _ptr(codes), _ptr(scales), _ptr(idx_k),
+                   None if idx_kscale is None else _vec(idx_kscale, torch.float32, total, "idx_kscale"), _ptr(workspace))
+    _same_device(a, latent, pos, codes, scales, seq, kv_offsets, page_table, weight, inv_freq, idx_proj, idx_inv_freq,
+                 idx_k, idx_kscale, workspace)
+    return a
+
+
+def append_rope(args: AppendArgs, stream=None) -> None:
+    """Cache append with norm and rotation on the way (csa2_append_rope)."""
+    _on_device(args, "append_rope")
+    _check(_lib.csa2_append_rope(ctypes.byref(args), _stream(stream)), "csa2_append_rope")
+
+
+def dequantize_kv(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, src_row: torch.Tensor | None = None,
+                  stream=None) -> None:
+    """Cache rows (src_row int64 [n], or rows 0 .. n-1) -> bf16 out [n][512]."""
+    _need(codes.dtype == torch.uint8 and scales.dtype == torch.uint8 and codes.shape[0] == scales.shape[0] and
+          codes.shape[1] == ROW_CODES and scales.shape[1] == ROW_SCALES, "codes uint8 [rows][256], scales uint8 [rows][32]")
+    _need(out.dtype == torch.bfloat16 and out.dim() == 2 and out.shape[1] == D, "out is bf16 [n][512]")
+    _need(out.device == codes.device == scales.device and out.device.index == torch.cuda.current_device(),
+          "dequantize_kv: the tensors are not on the current device")
+    _check(_lib.csa2_dequantize_kv(_ptr(codes), _ptr(scales), codes.shape[0],
+                                   _vec(src_row, torch.int64, out.shape[0], "src_row"), out.shape[0], _ptr(out),
+                                   _stream(stream)), "csa2_dequantize_kv")
+
+
+def cache_args(*, batch: int, max_n: int, kv_offsets: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+               q: torch.Tensor, out: torch.Tensor, q_per_seq: int = 1, q_pos: torch.Tensor | None = None, ratio: int = 1,
+               window: int = 0, sinks: int = 0, sm_scale: float = 1.0, lse: torch.Tensor | None = None,
+               page_table: torch.Tensor | None = None, page_rows: int = 0,
+               workspace: torch.Tensor | None = None) -> CacheArgs:
+    """Arguments of attend_cache.  q bf16 and out (bf16 or fp32) [batch * q_per_seq][16][512];
+    window 0: every visible position, else the last `window` and the first `sinks` ones; lse
+    fp32 [rows][16] or None; a paged cache as in layer_args."""
+    rows = batch * q_per_seq
+    _need(q.dtype == torch.bfloat16 and q.numel() == rows * HEADS * D, "q is bf16 [batch * q_per_seq][16][512]")
+    _need(out.numel() == rows * HEADS * D, "out is [batch * q_per_seq][16][512]")
+    _need(codes.dtype == torch.uint8 and scales.dtype == torch.uint8 and codes.shape[0] == scales.shape[0] and
+          codes.shape[-1] == ROW_CODES and scales.shape[-1] == ROW_SCALES, "codes uint8 [rows][256], scales uint8 [rows][32]")
+    _need(page_table is None or (page_table.dtype == torch.int32 and page_table.dim() == 2 and
+                                 page_table.shape[0] == batch), "page_table is int32 [batch][pages]")
+    a = CacheArgs(batch, q_per_seq, ratio, TYPES.get(out.dtype, -1), max_n, codes.shape[0], window, sinks,
+                  _vec(kv_offsets, torch.int64, batch + 1, "kv_offsets"), _vec(q_pos, torch.int64, batch, "q_pos"),
+                  _ptr(codes), _ptr(scales), _ptr(q), sm_scale, 0, _ptr(out),
+                  _vec(lse, torch.float32, rows * HEADS, "lse"), _ptr(page_table), int(page_rows) if page_table is not None else 0,
+                  0 if page_table is None else page_table.shape[1], _ptr(workspace),
+                  workspace.numel() if workspace is not None else 0)
+    _same_device(a, kv_offsets, codes, scales, q, out, q_pos, lse, page_table, workspace)
+    return a
+
+
+def cache_workspace_size(args: CacheArgs) -> int:
+    return _lib.csa2_cache_workspace_size(ctypes.byref(args))
+
+
+def attend_cache(args: CacheArgs, stream=None) -> None:
+    """Attention over the whole cache or a window of it (csa2_attend_cache)."""
+    _on_device(args, "attend_cache")
+    _check(_lib.csa2_attend_cache(ctypes.byref(args), _stream(stream)), "csa2_attend_cache")

@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "dense.cuh"
 #include "kernels.cuh"
 
 namespace csa2 {
@@ -73,6 +74,23 @@ WsLayout layer_layout(const csa2_layer_args* a) {
     const bool swa8 = a->swa_format == CSA2_SWA_FP8;
     L.n_split = attend_rows_split(rows, attend_rows_swa_tiles(a->swa_rows, a->q_pos != nullptr, swa8), swa8);
     L.total = off;
+    return L;
+}
+
+bool valid_type(int32_t t) { return t == CSA2_T_BF16 || t == CSA2_T_F16 || t == CSA2_T_F32; }
+
+// Workspace of csa2_attend_cache: two partials for each range of the tile list.
+struct CacheLayout {
+    int ranges = 1;
+    size_t meta = 0, part = 0, total = 0;
+};
+
+CacheLayout cache_layout(const csa2_cache_args* a) {
+    CacheLayout L;
+    L.ranges = cache_ranges(static_cast<int64_t>(a->batch) * a->q_per_seq, a->max_n, a->window, a->sinks);
+    L.meta = WS_HEADER;
+    L.part = L.meta + align_up(static_cast<size_t>(L.ranges) * 2 * sizeof(int32_t), 256);
+    L.total = L.part + align_up(static_cast<size_t>(L.ranges) * 2 * CACHE_PART_FLOATS * sizeof(float), 256);
     return L;
 }
 
@@ -211,7 +229,7 @@ bool make_idx_k_map(const uint8_t* idx_k, int64_t rows, int box_rows, CUtensorMa
 }  // namespace
 
 bool opt_in_smem(const void* kernel, int bytes) {
-    constexpr int kMaxDev = 64, kMaxKernels = 16;
+    constexpr int kMaxDev = 64, kMaxKernels = 32;
     static const void* kernels[kMaxKernels] = {};
     static bool done[kMaxKernels][kMaxDev] = {};
     static std::mutex mu;
@@ -532,6 +550,168 @@ csa2_status csa2_attend(const csa2_layer_args* a, void* stream) {
     const bool defer = st == CSA2_OK && a->ev_pool && a->mode == CSA2_MODE_FULL && a->want_pool;
     const csa2_status js = defer ? fork.defer(s, static_cast<cudaEvent_t>(a->ev_pool)) : fork.join(s);
     return st != CSA2_OK ? st : js;
+}
+
+csa2_status csa2_dequantize_kv(const uint8_t* codes, const uint8_t* scales, int64_t total_rows,
+                               const int64_t* src_row, int64_t n, uint16_t* out, void* stream) {
+    if (n < 0 || total_rows < 0) return CSA2_ERR_INVALID_ARG;
+    if (n == 0) return CSA2_OK;
+    if (!codes || !scales || !out || (!src_row && n > total_rows)) return CSA2_ERR_INVALID_ARG;
+    if (!aligned(codes, 8) || !aligned(out, 16) || !aligned(src_row, 8)) return CSA2_ERR_INVALID_ARG;
+    if (n > (int64_t(1) << 35)) return CSA2_ERR_UNSUPPORTED;
+    return launch_dequantize(codes, scales, total_rows, src_row, n, out, static_cast<cudaStream_t>(stream));
+}
+
+csa2_status csa2_norm_rope(const csa2_rope_args* a, void* stream) {
+    constexpr int32_t known = CSA2_ROPE_NORM | CSA2_ROPE_INVERSE | CSA2_ROPE_HALF;
+    if (!a || a->reserved0 != 0 || (a->flags & ~known) != 0 || a->rows < 0) return CSA2_ERR_INVALID_ARG;
+    if (!valid_type(a->in_type) || !valid_type(a->out_type)) return CSA2_ERR_INVALID_ARG;
+    if (a->heads < 1 || a->dim < 8 || a->dim % 8 != 0 || a->rope_dim < 0 || a->rope_dim > a->dim || a->rope_dim % 2 != 0)
+        return CSA2_ERR_INVALID_ARG;
+    if (a->heads > 1024 || a->dim > 1024) return CSA2_ERR_UNSUPPORTED;
+    if (!(a->eps >= 0.0f) || (a->weight && !(a->flags & CSA2_ROPE_NORM))) return CSA2_ERR_INVALID_ARG;
+    if (a->rows == 0) return CSA2_OK;
+    if (!a->x || !a->out || (a->rope_dim && (!a->pos || !a->inv_freq))) return CSA2_ERR_INVALID_ARG;
+    if (!aligned(a->x, 16) || !aligned(a->out, 16) || !aligned(a->weight, 16) || !aligned(a->pos, 8) ||
+        !aligned(a->inv_freq, 4))
+        return CSA2_ERR_INVALID_ARG;
+    const int xi = a->in_type == CSA2_T_F32 ? 4 : 8, oi = a->out_type == CSA2_T_F32 ? 4 : 8;   // elements per 16 B
+    if (a->x_row_stride < 0 || a->x_row_stride % xi != 0 || a->x_head_stride % xi != 0 || a->x_head_stride < 0 ||
+        a->out_row_stride < 0 || a->out_row_stride % oi != 0 || a->out_head_stride < 0 || a->out_head_stride % oi != 0)
+        return CSA2_ERR_INVALID_ARG;
+    // two vectors of out must not overlap: heads inside a row, or rows inside a head
+    if (a->heads > 1 && a->out_head_stride < a->dim) return CSA2_ERR_INVALID_ARG;
+    const int64_t row_span = (a->heads - 1) * a->out_head_stride + a->dim;
+    const int64_t col_span = (a->rows - 1) * a->out_row_stride + a->dim;
+    if (a->rows > 1 && !(a->out_row_stride >= row_span ||
+                         (a->out_row_stride >= a->dim && (a->heads == 1 || a->out_head_stride >= col_span))))
+        return CSA2_ERR_INVALID_ARG;
+    if (a->x == a->out && (a->in_type != a->out_type || a->x_row_stride != a->out_row_stride ||
+                           a->x_head_stride != a->out_head_stride))
+        return CSA2_ERR_INVALID_ARG;
+    RopeParams p;
+    p.rows = a->rows;
+    p.heads = a->heads;
+    p.dim = a->dim;
+    p.rope_dim = a->rope_dim;
+    p.norm = (a->flags & CSA2_ROPE_NORM) != 0;
+    p.inverse = (a->flags & CSA2_ROPE_INVERSE) != 0;
+    p.half = (a->flags & CSA2_ROPE_HALF) != 0 && a->rope_dim > 0;
+    p.x_row_stride = a->x_row_stride;
+    p.x_head_stride = a->x_head_stride;
+    p.out_row_stride = a->out_row_stride;
+    p.out_head_stride = a->out_head_stride;
+    p.x = a->x;
+    p.out = a->out;
+    p.pos = a->pos;
+    p.inv_freq = a->inv_freq;
+    p.weight = a->weight;
+    p.eps = a->eps;
+    return launch_norm_rope(p, a->in_type, a->out_type, static_cast<cudaStream_t>(stream));
+}
+
+csa2_status csa2_append_rope(const csa2_append_args* a, void* stream) {
+    constexpr int32_t known = CSA2_ROPE_NORM | CSA2_ROPE_HALF;
+    if (!a || (a->flags & ~known) != 0 || a->n < 0 || a->batch < 1 || !valid_type(a->in_type) || !(a->eps >= 0.0f))
+        return CSA2_ERR_INVALID_ARG;
+    if (a->rope_dim < 0 || a->rope_dim > D || a->rope_dim % 2 != 0 || a->idx_rope_dim < 0 || a->idx_rope_dim > IDX_DIM ||
+        a->idx_rope_dim % 2 != 0 || (a->weight && !(a->flags & CSA2_ROPE_NORM)))
+        return CSA2_ERR_INVALID_ARG;
+    if ((a->kv_offsets != nullptr) == (a->page_table != nullptr)) return CSA2_ERR_INVALID_ARG;
+    if (a->page_table && (a->page_rows < 128 || a->page_rows % 128 != 0 || a->page_rows > (1 << 24) || a->pages_per_seq < 1))
+        return CSA2_ERR_INVALID_ARG;
+    if (a->n == 0) return CSA2_OK;
+    if (!a->latent || !a->pos || !a->codes || !a->scales || a->total_rows < 1 || (!a->seq && a->n > a->batch))
+        return CSA2_ERR_INVALID_ARG;
+    if ((a->rope_dim && !a->inv_freq) || (a->idx_proj && (!a->idx_k || !a->idx_kscale)) ||
+        (a->idx_proj && a->idx_rope_dim && !a->idx_inv_freq))
+        return CSA2_ERR_INVALID_ARG;
+    const int li = a->in_type == CSA2_T_F32 ? 4 : 8;
+    if (a->latent_stride < D || a->latent_stride % li != 0 ||
+        (a->idx_proj && (a->idx_stride < IDX_DIM || a->idx_stride % 2 != 0)))
+        return CSA2_ERR_INVALID_ARG;
+    if (!aligned(a->latent, 16) || !aligned(a->idx_proj, 8) || !aligned(a->weight, 16) || !aligned(a->pos, 8) ||
+        !aligned(a->seq, 4) || !aligned(a->kv_offsets, 8) || !aligned(a->page_table, 4) || !aligned(a->inv_freq, 4) ||
+        !aligned(a->idx_inv_freq, 4) || !aligned(a->codes, 8) || !aligned(a->idx_k, 2) || !aligned(a->idx_kscale, 4))
+        return CSA2_ERR_INVALID_ARG;
+    if (a->workspace && !aligned(a->workspace, 256)) return CSA2_ERR_WORKSPACE;
+    AppendParams p;
+    p.n = a->n;
+    p.batch = a->batch;
+    p.rope_dim = a->rope_dim;
+    p.idx_rope_dim = a->idx_rope_dim;
+    p.norm = (a->flags & CSA2_ROPE_NORM) != 0;
+    p.half = (a->flags & CSA2_ROPE_HALF) != 0;
+    p.eps = a->eps;
+    p.latent_stride = a->latent_stride;
+    p.idx_stride = a->idx_stride;
+    p.total_rows = a->total_rows;
+    p.latent = a->latent;
+    p.idx_proj = a->idx_proj;
+    p.seq = a->seq;
+    p.pos = a->pos;
+    p.kv_offsets = a->kv_offsets;
+    p.rows = RowMap{a->page_table, a->page_rows, a->pages_per_seq};
+    p.inv_freq = a->inv_freq;
+    p.idx_inv_freq = a->idx_inv_freq;
+    p.weight = a->weight;
+    p.codes = a->codes;
+    p.scales = a->scales;
+    p.idx_k = a->idx_k;
+    p.idx_kscale = a->idx_kscale;
+    p.err = static_cast<unsigned*>(a->workspace);
+    return launch_append_rope(p, a->in_type, static_cast<cudaStream_t>(stream));
+}
+
+size_t csa2_cache_workspace_size(const csa2_cache_args* a) {
+    if (!a || a->batch < 1 || a->q_per_seq < 1 || a->max_n < 1) return 0;
+    return cache_layout(a).total;
+}
+
+csa2_status csa2_attend_cache(const csa2_cache_args* a, void* stream) {
+    if (!a) return CSA2_ERR_INVALID_ARG;
+    if (a->batch < 1 || a->q_per_seq < 1 || a->q_per_seq > 65536 || (a->ratio != 1 && a->ratio != 2))
+        return CSA2_ERR_INVALID_ARG;
+    if (a->out_type != CSA2_T_BF16 && a->out_type != CSA2_T_F32)
+        return valid_type(a->out_type) ? CSA2_ERR_UNSUPPORTED : CSA2_ERR_INVALID_ARG;
+    if (a->reserved0 != 0 || a->max_n < 1 || a->total_n < 1 || a->total_n > INT32_MAX || a->window < 0 || a->sinks < 0)
+        return CSA2_ERR_INVALID_ARG;
+    if (a->max_n > INT32_MAX || static_cast<int64_t>(a->batch) * a->q_per_seq > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
+    if (!a->kv_offsets || !a->codes || !a->scales || !a->q || !a->out) return CSA2_ERR_INVALID_ARG;
+    if (!(a->sm_scale - a->sm_scale == 0.0f)) return CSA2_ERR_INVALID_ARG;          // finite
+    if (!aligned(a->codes, 16) || !aligned(a->scales, 16) || !aligned(a->q, 16) || !aligned(a->out, 16) ||
+        !aligned(a->lse, 4) || !aligned(a->kv_offsets, 8) || !aligned(a->q_pos, 8) || !aligned(a->page_table, 4))
+        return CSA2_ERR_INVALID_ARG;
+    if (a->page_table) {
+        if (a->page_rows < 128 || a->page_rows % 128 != 0 || a->page_rows > (1 << 24)) return CSA2_ERR_INVALID_ARG;
+        if (a->pages_per_seq < ceil_div(a->max_n, a->page_rows)) return CSA2_ERR_INVALID_ARG;
+    }
+    const CacheLayout L = cache_layout(a);
+    if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < L.total) return CSA2_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+    CacheParams p;
+    p.batch = a->batch;
+    p.q_per_seq = a->q_per_seq;
+    p.ratio = a->ratio;
+    p.out_f32 = a->out_type == CSA2_T_F32;
+    p.max_n = a->max_n;
+    p.total_n = a->total_n;
+    p.window = a->window;
+    p.sinks = a->sinks;
+    p.kv_offsets = a->kv_offsets;
+    p.q_pos = a->q_pos;
+    p.codes = a->codes;
+    p.scales = a->scales;
+    p.q = a->q;
+    p.sm_scale = a->sm_scale;
+    p.out = a->out;
+    p.lse = a->lse;
+    p.rows = RowMap{a->page_table, a->page_rows, a->pages_per_seq};
+    p.err = reinterpret_cast<unsigned*>(ws);
+    p.meta = reinterpret_cast<int32_t*>(ws + L.meta);
+    p.part = reinterpret_cast<float*>(ws + L.part);
+    p.ranges = L.ranges;
+    return launch_attend_cache(p, static_cast<cudaStream_t>(stream));
 }
 
 csa2_status csa2_set_wait_limit(void* workspace, uint32_t polls, void* stream) {

@@ -1,0 +1,78 @@
+// Launchers of the dense-cache operators: read-back, norm and rotation, append with both,
+// attention over the whole cache.
+#pragma once
+
+#include "common.cuh"
+
+namespace csa2 {
+
+// FP4 rows back to bf16 (rows outside [0, total_rows) give zeros).
+csa2_status launch_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t total_rows, const int64_t* src_row,
+                              int64_t n, uint16_t* out, cudaStream_t stream);
+
+// Head norm and rotation of [rows][heads][dim] vectors (csa2_norm_rope).
+struct RopeParams {
+    int64_t rows;
+    int heads, dim, rope_dim;
+    int norm, inverse, half;
+    int64_t x_row_stride, x_head_stride, out_row_stride, out_head_stride;
+    const void* x;
+    void* out;
+    const int64_t* pos;
+    const float* inv_freq;
+    const float* weight;
+    float eps;
+};
+csa2_status launch_norm_rope(const RopeParams& p, int in_type, int out_type, cudaStream_t stream);
+
+// Cache append with norm and rotation (csa2_append_rope).
+struct AppendParams {
+    int64_t n;
+    int batch, rope_dim, idx_rope_dim;
+    int norm, half;
+    float eps;
+    int64_t latent_stride, idx_stride, total_rows;
+    const void* latent;
+    const float* idx_proj;
+    const int32_t* seq;
+    const int64_t* pos;
+    const int64_t* kv_offsets;
+    RowMap rows;
+    const float* inv_freq;
+    const float* idx_inv_freq;
+    const float* weight;
+    uint8_t* codes;
+    uint8_t* scales;
+    uint8_t* idx_k;
+    float* idx_kscale;
+    unsigned* err;            // device error word, or nullptr
+};
+csa2_status launch_append_rope(const AppendParams& p, int in_type, cudaStream_t stream);
+
+// Attention over the cache without an index (csa2_attend_cache): the visible tiles of all
+// rows form one list, cut into CACHE_CTAS-many equal ranges; a row cut by a range's end is
+// joined from the ranges' partials.
+struct CacheParams {
+    int batch, q_per_seq, ratio, out_f32;
+    int64_t max_n, total_n, window, sinks;
+    const int64_t* kv_offsets;
+    const int64_t* q_pos;
+    const uint8_t* codes;
+    const uint8_t* scales;
+    const uint16_t* q;
+    float sm_scale;
+    void* out;
+    float* lse;
+    RowMap rows;
+    unsigned* err;            // workspace header
+    int32_t* meta;            // [ranges][2] rows of a range's two partials (-1: none)
+    float* part;              // [ranges][2] partials: m[16], l[16], O[16][512]
+    int ranges;
+};
+constexpr int CACHE_TILE = 128;                                  // positions per tile
+constexpr int CACHE_MAX_RANGES = 148;                            // one CTA per SM
+constexpr int CACHE_PART_FLOATS = 2 * HEADS + HEADS * D;
+int cache_ranges(int64_t rows, int64_t max_n, int64_t window, int64_t sinks);
+csa2_status launch_attend_cache(const CacheParams& p, cudaStream_t stream);
+
+}  // namespace csa2

@@ -10,20 +10,14 @@
 // The rounding decisions use IEEE fp32 division (never a reciprocal multiply): both
 // operands carry at most 8 significant bits, so the fp32 quotient lands exactly on a
 // rounding midpoint iff the exact quotient does, and never crosses one.
-#include "common.cuh"
+#include <cuda_fp4.h>
+
+#include "dense.cuh"
+#include "row_formats.cuh"
 
 namespace csa2 {
 
 namespace {
-
-// Round-to-nearest-even of a float64 value to bf16, through a round-to-odd float32
-// intermediate (16 spare bits make the second rounding exact).
-__device__ __forceinline__ uint16_t f64_to_bf16_rne(double m) {
-    float f = __double2float_rz(m);
-    if (static_cast<double>(f) != m) f = __uint_as_float(__float_as_uint(f) | 1u);
-    __nv_bfloat16 h = __float2bfloat16_rn(f);
-    return *reinterpret_cast<uint16_t*>(&h);
-}
 
 __device__ __forceinline__ void unpack8(const uint4& v, uint16_t (&h)[16], int base) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -77,9 +71,7 @@ quantize_kernel(const uint16_t* __restrict__ x, int64_t n_out, int ratio,
 }
 
 // Cache append of new positions: warp per row.  Lane l quantises channels 16l..16l+15
-// of the main-KV row (as above) and indexer values 2l, 2l+1: kscale = amax / 448 and
-// code = sign | E4M3 RNE saturating of |k / kscale|, both quotients IEEE fp32; an
-// all-zero row gets kscale 0 and zero codes.
+// of the main-KV row (as above) and indexer values 2l, 2l+1 (store_idx_row).
 __global__ void __launch_bounds__(256)
 append_kernel(const uint16_t* __restrict__ latent, const float* __restrict__ proj, int64_t n,
               const int64_t* __restrict__ dst_row, uint8_t* __restrict__ codes,
@@ -96,21 +88,62 @@ append_kernel(const uint16_t* __restrict__ latent, const float* __restrict__ pro
     store_group(h, codes + out_row * ROW_CODES + lane * 8, scales + out_row * ROW_SCALES + lane);
 
     const float2 k = __ldg(reinterpret_cast<const float2*>(proj + row * IDX_DIM) + lane);
-    float amax = fmaxf(fabsf(k.x), fabsf(k.y));
+    store_idx_row(k, lane, idx_k + out_row * IDX_DIM, idx_kscale + out_row);
+}
+
+// FP4 rows back to bf16: one lane per 16-channel group, 8 code bytes and a scale in, 32
+// bytes out; four rows per warp in flight.  e2m1 x e4m3 has at most 6 significant bits, so
+// the fp32 product and its bf16 rounding are both exact.
+constexpr int DQ_ROWS = 4;
+
+__global__ void __launch_bounds__(256)
+dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t total_rows,
+                  const int64_t* __restrict__ src_row, int64_t n, uint16_t* __restrict__ out) {
+    const int lane = threadIdx.x & 31;
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32) * DQ_ROWS;
+    uint2 c[DQ_ROWS];
+    uint32_t sc[DQ_ROWS];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
-    const float ks = amax / 448.0f;
-    uint32_t c0 = 0, c1 = 0;
-    if (ks > 0.0f) {
-        const float q0 = k.x / ks, q1 = k.y / ks;
-        c0 = (signbit(q0) ? 0x80u : 0u) | e4m3_encode_rne_sat(fabsf(q0));
-        c1 = (signbit(q1) ? 0x80u : 0u) | e4m3_encode_rne_sat(fabsf(q1));
+    for (int r = 0; r < DQ_ROWS; ++r) {
+        c[r] = make_uint2(0u, 0u);
+        sc[r] = 0u;
+        if (first + r < n) {
+            const int64_t row = src_row ? __ldg(src_row + first + r) : first + r;
+            if (row >= 0 && row < total_rows) {
+                c[r] = __ldg(reinterpret_cast<const uint2*>(codes + row * ROW_CODES) + lane);
+                sc[r] = __ldg(scales + row * ROW_SCALES + lane);
+            }
+        }
     }
-    reinterpret_cast<uint16_t*>(idx_k + out_row * IDX_DIM)[lane] = static_cast<uint16_t>(c0 | (c1 << 8));
-    if (lane == 0) idx_kscale[out_row] = ks;
+#pragma unroll
+    for (int r = 0; r < DQ_ROWS; ++r) {
+        if (first + r >= n) return;
+        const float s = e4m3_to_float(static_cast<uint8_t>(sc[r]));
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t byte = ((i < 4 ? c[r].x : c[r].y) >> (8 * (i & 3))) & 0xFFu;
+            const __half2_raw hr = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
+            const float2 f = __half22float2(__half2(hr));
+            const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * s, f.y * s);
+            w[i] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(out + (first + r) * D + lane * GROUP);
+        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 
 }  // namespace
+
+csa2_status launch_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t total_rows, const int64_t* src_row,
+                              int64_t n, uint16_t* out, cudaStream_t stream) {
+    if (n == 0) return CSA2_OK;
+    const int rows_per_block = 8 * DQ_ROWS;
+    dequantize_kernel<<<static_cast<unsigned>(ceil_div(n, rows_per_block)), 256, 0, stream>>>(codes, scales, total_rows,
+                                                                                           src_row, n, out);
+    return check_launch("dequantize_kernel");
+}
 
 csa2_status launch_append(const uint16_t* latent, const float* proj, int64_t n, const int64_t* dst_row,
                           uint8_t* codes, uint8_t* scales, uint8_t* idx_k, float* idx_kscale,

@@ -1,0 +1,413 @@
+// Head norm and rotary positions: queries (norm_rope_kernel) and the cache append with
+// both on the way (append_rope_kernel).  Neither is described by the pages; the append
+// writes the pages' FP4 main-KV row and FP8 indexer row (quantize.cu has the plain append).
+//
+//   y = x * w / sqrt(mean(x^2) + eps);  (u, v) -> (u cos a - v sin a, v cos a + u sin a),
+//   a = position * inv_freq.
+//
+// The angle is formed in 64 bits and reduced there to a fraction of a turn, so a position
+// of 2^30 still has its angle to 2^-22 of a turn; only then does sincospi see it.
+#include "dense.cuh"
+#include "row_formats.cuh"
+
+namespace csa2 {
+
+namespace {
+
+constexpr double INV_TWO_PI = 0.15915494309189533577;
+
+// Fraction of a turn, in [-1/2, 1/2], of the angle pos * inv_freq (radians).
+__device__ __forceinline__ double turn_fraction(int64_t pos, float inv_freq) {
+    const double t = static_cast<double>(pos) * static_cast<double>(inv_freq) * INV_TWO_PI;
+    return t - rint(t);
+}
+
+template <int T> struct Elem;
+template <> struct Elem<CSA2_T_BF16> { using type = __nv_bfloat16; };
+template <> struct Elem<CSA2_T_F16> { using type = __half; };
+template <> struct Elem<CSA2_T_F32> { using type = float; };
+
+// 8 elements -> fp32 (16-byte loads).
+template <int T>
+__device__ __forceinline__ void load8(const typename Elem<T>::type* p, float (&v)[8]) {
+    if constexpr (T == CSA2_T_F32) {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (T == CSA2_T_BF16) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+    }
+}
+
+template <int T>
+__device__ __forceinline__ void store8(typename Elem<T>::type* p, const float (&v)[8]) {
+    if constexpr (T == CSA2_T_F32) {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (T == CSA2_T_BF16) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Queries.  A block takes rows_per_block tokens: first their cos / sin tables (one per
+// token, shared by its heads), then their vectors, `lanes` lanes (a power of two) per
+// vector and 8 channels per lane and item.  The half-split pairing reaches across lanes,
+// so there the vector goes through shared memory once.
+constexpr int NR_THREADS = 256;
+constexpr int NR_MAX_PAIRS = 2048;             // cos / sin pairs of a block (16 KB)
+
+// Pairs of a block's table, rounded up so that the vectors behind it start 16-byte aligned.
+__host__ __device__ __forceinline__ int table_pairs(int rows_per_block, int pairs) {
+    return (rows_per_block * pairs + 1) & ~1;
+}
+
+template <int TI, int TO, int ITEMS, bool HALF>
+__global__ void __launch_bounds__(NR_THREADS)
+norm_rope_kernel(RopeParams p, int rows_per_block, int lanes) {
+    extern __shared__ float2 nr_smem[];        // [rows_per_block][rope_dim / 2], then vectors
+    const int pairs = p.rope_dim / 2;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows_per_block;
+    const int n_rows = static_cast<int>(min(static_cast<int64_t>(rows_per_block), p.rows - row0));
+    for (int i = threadIdx.x; i < n_rows * pairs; i += NR_THREADS) {
+        const int r = i / pairs, k = i - r * pairs;
+        const float t = 2.0f * static_cast<float>(turn_fraction(p.pos[row0 + r], p.inv_freq[k]));
+        float s, c;
+        sincospif(t, &s, &c);
+        nr_smem[i] = make_float2(c, p.inverse ? -s : s);
+    }
+    if (pairs) __syncthreads();
+
+    const int sub = threadIdx.x / lanes, sl = threadIdx.x % lanes, subs = NR_THREADS / lanes;
+    float* stage = reinterpret_cast<float*>(nr_smem + table_pairs(rows_per_block, pairs)) + sub * p.dim;
+    const int start = p.dim - p.rope_dim;
+    const int total = n_rows * p.heads;
+    // every thread makes the same number of turns: the shuffles and barriers below are
+    // whole-warp, and a vector past the end is worked on as the last one and not stored
+    for (int v0 = 0; v0 < total; v0 += subs) {
+        const int vi = min(v0 + sub, total - 1);
+        const bool live = v0 + sub < total;
+        const int r = vi / p.heads, h = vi - r * p.heads;
+        const auto* x = static_cast<const typename Elem<TI>::type*>(p.x) + (row0 + r) * p.x_row_stride +
+                        h * p.x_head_stride;
+        float y[ITEMS][8];
+        float ss = 0.0f;
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) {
+            const int c = (it * lanes + sl) * 8;
+            if (c < p.dim) {
+                load8<TI>(x + c, y[it]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[it][j] = 0.0f;
+            }
+        }
+        if (p.norm) {
+#pragma unroll
+            for (int it = 0; it < ITEMS; ++it)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ss = fmaf(y[it][j], y[it][j], ss);
+            for (int o = lanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+            const float rs = 1.0f / sqrtf(ss / static_cast<float>(p.dim) + p.eps);
+#pragma unroll
+            for (int it = 0; it < ITEMS; ++it) {
+                const int c = (it * lanes + sl) * 8;
+                if (p.weight != nullptr && c < p.dim) {
+                    float w[8];
+                    load8<CSA2_T_F32>(p.weight + c, w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[it][j] *= rs * w[j];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[it][j] *= rs;
+                }
+            }
+        }
+        const float2* cs = nr_smem + r * pairs;
+        if constexpr (HALF) {
+#pragma unroll
+            for (int it = 0; it < ITEMS; ++it) {
+                const int c = (it * lanes + sl) * 8;
+                if (c < p.dim) store8<CSA2_T_F32>(stage + c, y[it]);
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) {
+            const int c = (it * lanes + sl) * 8;
+            if (c >= p.dim) continue;
+            if (c + 8 > start) {
+                if constexpr (HALF) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int k = c + j - start;
+                        if (k >= 0) {
+                            const bool second = k >= pairs;
+                            const float2 a = cs[second ? k - pairs : k];
+                            const float other = stage[second ? c + j - pairs : c + j + pairs];
+                            y[it][j] = second ? y[it][j] * a.x + other * a.y : y[it][j] * a.x - other * a.y;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        if (c + j >= start) {
+                            const float2 a = cs[(c + j - start) >> 1];
+                            const float u = y[it][j], v = y[it][j + 1];
+                            y[it][j] = u * a.x - v * a.y;
+                            y[it][j + 1] = v * a.x + u * a.y;
+                        }
+                    }
+                }
+            }
+            if (live) {
+                auto* o = static_cast<typename Elem<TO>::type*>(p.out) + (row0 + r) * p.out_row_stride +
+                          h * p.out_head_stride;
+                store8<TO>(o + c, y[it]);
+            }
+        }
+        if constexpr (HALF) __syncwarp();
+    }
+}
+
+// ------------------------------------------------------------------ append
+
+// bf16 bits of hi + lo, |lo| <= half a unit of hi, rounded to nearest even: a bf16
+// rounding boundary is an fp32 number, so only hi exactly on it needs lo's sign.
+__device__ __forceinline__ uint16_t round_bf16(float hi, float lo) {
+    uint32_t b = __float_as_uint(hi);
+    if ((b & 0xFFFFu) == 0x8000u && lo != 0.0f) b += (lo > 0.0f) == (hi > 0.0f) ? 1u : 0xFFFFFFFFu;
+    const __nv_bfloat16 h = __float2bfloat16_rn(__uint_as_float(b));
+    return *reinterpret_cast<const uint16_t*>(&h);
+}
+
+constexpr int AR_WARPS = 8;
+
+// One warp per token, one lane per 16-channel group (as in quantize.cu).  The FP4 codes
+// change by a whole step at a border, so the bf16 value they are made of is the real
+// number's rounding: the sum of squares and 1/sqrt in 64 bits, x * (w * r) as an fp32 pair
+// hi + lo (its error ~2^-45), the rotated channels in 64 bits.  Shared memory per warp:
+// 256 (cos, sin) double pairs and, for the half-split pairing, the 512 normed channels.
+template <int TI>
+__global__ void __launch_bounds__(32 * AR_WARPS)
+append_rope_kernel(AppendParams p) {
+    extern __shared__ double2 ar_smem[];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * AR_WARPS + warp;
+    if (i >= p.n) return;
+    const int64_t pos = p.pos[i];
+    if (pos < 0) return;
+    const int64_t b = p.seq ? p.seq[i] : i;
+    int64_t row = -1;
+    if (b >= 0 && b < p.batch) {
+        if (p.rows.page_table) {
+            if (pos < static_cast<int64_t>(p.rows.pages_per_seq) * p.rows.page_rows) {
+                const int64_t pg = __ldg(p.rows.page_table + b * p.rows.pages_per_seq + pos / p.rows.page_rows);
+                if (pg >= 0) row = pg * p.rows.page_rows + pos % p.rows.page_rows;
+            }
+        } else {
+            const int64_t o = p.kv_offsets[b];
+            if (o >= 0 && pos < p.kv_offsets[b + 1] - o) row = o + pos;
+        }
+    }
+    if (row < 0 || row >= p.total_rows) {
+        if (lane == 0 && p.err) atomicOr(p.err, ERR_DEVICE);
+        return;
+    }
+
+    const int pairs = p.rope_dim / 2;
+    double2* cs = ar_smem + warp * (pairs + (p.half && pairs ? D / 2 : 0));
+    for (int k = lane; k < pairs; k += 32) {
+        double s, c;
+        sincospi(2.0 * turn_fraction(pos, p.inv_freq[k]), &s, &c);
+        cs[k] = make_double2(c, s);
+    }
+
+    const auto* src = static_cast<const typename Elem<TI>::type*>(p.latent) + i * p.latent_stride + lane * GROUP;
+    float x[16];
+    {
+        float a[8];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            load8<TI>(src + 8 * q, a);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[8 * q + j] = a[j];
+        }
+    }
+    float hi[16], lo[16];
+    if (p.norm) {
+        double ss = 0.0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) ss = fma(static_cast<double>(x[j]), static_cast<double>(x[j]), ss);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        const double r = 1.0 / sqrt(ss / D + static_cast<double>(p.eps));
+        const float rh = static_cast<float>(r), rl = static_cast<float>(r - static_cast<double>(rh));
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float w = p.weight ? __ldg(p.weight + lane * GROUP + j) : 1.0f;
+            const float ph = w * rh, pl = fmaf(w, rl, fmaf(w, rh, -ph));
+            const float yh = x[j] * ph, yl = fmaf(x[j], pl, fmaf(x[j], ph, -yh));
+            hi[j] = yh + yl;
+            lo[j] = yl - (hi[j] - yh);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            hi[j] = x[j];
+            lo[j] = 0.0f;
+        }
+    }
+
+    uint16_t h[16];
+    const int start = D - p.rope_dim;
+    if (pairs && p.half) {                                  // partners across lanes: by shared memory
+        double* y = reinterpret_cast<double*>(cs + pairs);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[lane * GROUP + j] = static_cast<double>(hi[j]) + static_cast<double>(lo[j]);
+    }
+    __syncwarp();
+    if (pairs && lane * GROUP + GROUP > start) {
+        const double* y = reinterpret_cast<const double*>(cs + pairs);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            const int k = lane * GROUP + j - start;        // even: start is even
+            if (k < 0) {
+                h[j] = round_bf16(hi[j], lo[j]);
+                h[j + 1] = round_bf16(hi[j + 1], lo[j + 1]);
+            } else if (!p.half) {
+                const double u = static_cast<double>(hi[j]) + static_cast<double>(lo[j]);
+                const double v = static_cast<double>(hi[j + 1]) + static_cast<double>(lo[j + 1]);
+                const double2 a = cs[k >> 1];
+                h[j] = f64_to_bf16_rne(u * a.x - v * a.y);
+                h[j + 1] = f64_to_bf16_rne(v * a.x + u * a.y);
+            } else {
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    const int kk = k + d;
+                    const bool second = kk >= pairs;
+                    const double2 a = cs[second ? kk - pairs : kk];
+                    const double me = y[start + kk], other = y[start + (second ? kk - pairs : kk + pairs)];
+                    h[j + d] = f64_to_bf16_rne(second ? me * a.x + other * a.y : me * a.x - other * a.y);
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) h[j] = round_bf16(hi[j], lo[j]);
+    }
+    uint2 v;
+    const uint8_t sc = nvfp4_group(h, v);
+    *reinterpret_cast<uint2*>(p.codes + row * ROW_CODES + lane * 8) = v;
+    p.scales[row * ROW_SCALES + lane] = sc;
+
+    if (!p.idx_proj) return;
+    // indexer row: lane l holds values 2l, 2l+1 (a pair of the interleaved rotation)
+    float2 k = *reinterpret_cast<const float2*>(p.idx_proj + i * p.idx_stride + 2 * lane);
+    const int ip = p.idx_rope_dim / 2, c0 = 2 * lane - (IDX_DIM - p.idx_rope_dim);
+    if (ip) {
+        if (!p.half) {
+            float s = 0.0f, c = 1.0f;
+            if (c0 >= 0) sincospif(2.0f * static_cast<float>(turn_fraction(pos, p.idx_inv_freq[c0 >> 1])), &s, &c);
+            k = make_float2(k.x * c - k.y * s, k.y * c + k.x * s);
+        } else {
+            float out[2];
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                const int kk = c0 + d;
+                const bool second = kk >= ip;
+                const int partner = (IDX_DIM - p.idx_rope_dim) + (kk < 0 ? 0 : second ? kk - ip : kk + ip);
+                const float o0 = __shfl_sync(0xFFFFFFFFu, k.x, partner >> 1);
+                const float o1 = __shfl_sync(0xFFFFFFFFu, k.y, partner >> 1);
+                const float other = (partner & 1) ? o1 : o0, me = d ? k.y : k.x;
+                float s = 0.0f, c = 1.0f;
+                if (kk >= 0)
+                    sincospif(2.0f * static_cast<float>(turn_fraction(pos, p.idx_inv_freq[second ? kk - ip : kk])), &s,
+                              &c);
+                out[d] = second ? me * c + other * s : me * c - other * s;
+            }
+            k = make_float2(out[0], out[1]);
+        }
+    }
+    const float2 kr = k;
+    store_idx_row(kr, lane, p.idx_k + row * IDX_DIM, p.idx_kscale + row);
+}
+
+template <int TI, int TO, int ITEMS>
+csa2_status launch_norm(const RopeParams& p, int rows_per_block, int lanes, int smem, cudaStream_t stream) {
+    const unsigned grid = static_cast<unsigned>(ceil_div(p.rows, rows_per_block));
+    if (p.half) norm_rope_kernel<TI, TO, ITEMS, true><<<grid, NR_THREADS, smem, stream>>>(p, rows_per_block, lanes);
+    else norm_rope_kernel<TI, TO, ITEMS, false><<<grid, NR_THREADS, smem, stream>>>(p, rows_per_block, lanes);
+    return check_launch("norm_rope_kernel");
+}
+
+template <int TI, int TO>
+csa2_status launch_norm_items(const RopeParams& p, int rpb, int lanes, int smem, cudaStream_t stream) {
+    const int items = (p.dim / 8 + lanes - 1) / lanes;
+    if (items <= 1) return launch_norm<TI, TO, 1>(p, rpb, lanes, smem, stream);
+    if (items <= 2) return launch_norm<TI, TO, 2>(p, rpb, lanes, smem, stream);
+    return launch_norm<TI, TO, 4>(p, rpb, lanes, smem, stream);
+}
+
+template <int TI>
+csa2_status launch_norm_out(const RopeParams& p, int out_type, int rpb, int lanes, int smem, cudaStream_t stream) {
+    if (out_type == CSA2_T_BF16) return launch_norm_items<TI, CSA2_T_BF16>(p, rpb, lanes, smem, stream);
+    if (out_type == CSA2_T_F16) return launch_norm_items<TI, CSA2_T_F16>(p, rpb, lanes, smem, stream);
+    return launch_norm_items<TI, CSA2_T_F32>(p, rpb, lanes, smem, stream);
+}
+
+}  // namespace
+
+csa2_status launch_norm_rope(const RopeParams& p, int in_type, int out_type, cudaStream_t stream) {
+    if (p.rows == 0) return CSA2_OK;
+    int lanes = 1;
+    while (lanes < 32 && lanes * 8 < p.dim) lanes *= 2;
+    const int subs = NR_THREADS / lanes, pairs = p.rope_dim / 2;
+    // enough vectors for every sub-warp of a block, within the table's share of shared memory
+    int rpb = static_cast<int>(ceil_div(subs, p.heads));
+    if (pairs && rpb * pairs > NR_MAX_PAIRS) rpb = NR_MAX_PAIRS / pairs;
+    const int smem = table_pairs(rpb, pairs) * static_cast<int>(sizeof(float2)) + (p.half ? subs * p.dim * 4 : 0);
+    if (ceil_div(p.rows, rpb) > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
+    if (in_type == CSA2_T_BF16) return launch_norm_out<CSA2_T_BF16>(p, out_type, rpb, lanes, smem, stream);
+    if (in_type == CSA2_T_F16) return launch_norm_out<CSA2_T_F16>(p, out_type, rpb, lanes, smem, stream);
+    return launch_norm_out<CSA2_T_F32>(p, out_type, rpb, lanes, smem, stream);
+}
+
+csa2_status launch_append_rope(const AppendParams& p, int in_type, cudaStream_t stream) {
+    if (p.n == 0) return CSA2_OK;
+    const int pairs = p.rope_dim / 2;
+    const int smem = AR_WARPS * (pairs + (p.half && pairs ? D / 2 : 0)) * static_cast<int>(sizeof(double2));
+    const int64_t grid = ceil_div(p.n, AR_WARPS);
+    if (grid > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
+    const void* fn = in_type == CSA2_T_BF16  ? reinterpret_cast<const void*>(append_rope_kernel<CSA2_T_BF16>)
+                     : in_type == CSA2_T_F16 ? reinterpret_cast<const void*>(append_rope_kernel<CSA2_T_F16>)
+                                             : reinterpret_cast<const void*>(append_rope_kernel<CSA2_T_F32>);
+    constexpr int MAX_SMEM = AR_WARPS * (D / 2 + D / 2) * static_cast<int>(sizeof(double2));
+    if (smem > 48 * 1024 && !opt_in_smem(fn, MAX_SMEM)) return check_launch("append_rope_kernel smem attribute");
+    void* args[] = {const_cast<AppendParams*>(&p)};
+    cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(32 * AR_WARPS), args, smem, stream);
+    return check_launch("append_rope_kernel");
+}
+
+}  // namespace csa2

@@ -405,6 +405,152 @@ csa2_status csa2_check_device_status(void* workspace, void* stream);
  * it (it is part of this library's failure handling, not of the method). */
 csa2_status csa2_set_wait_limit(void* workspace, uint32_t polls, void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Dense use of the FP4 cache.  The pages attend sparsely (Top-512); these four calls are
+ * what a decoder needs around and beside that: the query's and the latent's head norm and
+ * rotary position embedding, the cache append with both on the way, the read-back of
+ * cache rows, and attention of new tokens over every position of the cache, or over a
+ * sliding window of it plus the first positions.
+ *
+ * Rotation shared by csa2_norm_rope and csa2_append_rope: the last `rope_dim` channels of
+ * a vector of `dim` are r/2 pairs (r = rope_dim, even); pair i of the vector at position p
+ * is turned by the angle p * inv_freq[i],
+ *   (u, v) -> (u cos a - v sin a, v cos a + u sin a),
+ * u and v being channels 2i, 2i+1 of those r (or i, i + r/2 with CSA2_ROPE_HALF).  The
+ * angle is formed and reduced in 64 bits, so far positions lose nothing.
+ * Norm: y = x * w / sqrt(mean(x^2) + eps) over the vector's `dim` channels (w = 1 when
+ * `weight` is NULL), before the rotation.
+ * ------------------------------------------------------------------------------- */
+#define CSA2_T_BF16 0
+#define CSA2_T_F16  1
+#define CSA2_T_F32  2
+
+#define CSA2_ROPE_NORM    1   /* RMS norm of each vector first                          */
+#define CSA2_ROPE_INVERSE 2   /* turn by -angle (takes an attention output, whose values
+                                 are rotated rows, back to its query's frame)           */
+#define CSA2_ROPE_HALF    4   /* pairs (i, i + r/2) instead of (2i, 2i+1)               */
+
+typedef struct csa2_rope_args {
+    int64_t rows;               /* tokens (>= 0; 0 enqueues nothing)                    */
+    int32_t heads;              /* vectors per token, 1 .. 1024                         */
+    int32_t dim;                /* channels per vector: a multiple of 8, 8 .. 1024      */
+    int32_t rope_dim;           /* rotated channels: even, 0 (no rotation) .. dim       */
+    int32_t in_type;            /* CSA2_T_* of x                                        */
+    int32_t out_type;           /* CSA2_T_* of out (one rounding, to nearest even)      */
+    int32_t flags;              /* CSA2_ROPE_* bits                                     */
+    int64_t x_row_stride;       /* elements between tokens / heads of x and out; every  */
+    int64_t x_head_stride;      /*   vector must start 16-byte aligned                  */
+    int64_t out_row_stride;
+    int64_t out_head_stride;
+    const void* x;              /* [rows][heads][dim] with those strides                */
+    void* out;                  /* same shape; may be x itself with the same type and
+                                   strides, must not overlap it otherwise               */
+    const int64_t* pos;         /* [rows] position of each token (rope_dim > 0)         */
+    const float* inv_freq;      /* [rope_dim/2] (rope_dim > 0)                          */
+    const float* weight;        /* [dim] (16-byte aligned) or NULL (CSA2_ROPE_NORM only) */
+    float eps;                  /* >= 0                                                 */
+    int32_t reserved0;          /* must be 0                                            */
+} csa2_rope_args;
+
+/* csa2_norm_rope — head norm and rotary positions of queries (or indexer queries), or with
+ * CSA2_ROPE_INVERSE and no norm the way back for attention outputs, in one pass. */
+csa2_status csa2_norm_rope(const csa2_rope_args* a, void* stream);
+
+/* csa2_append_rope — the cache append of csa2_append_kv with norm and rotation of the
+ * latent on the way, addressed by (sequence, position) instead of by row.  Token i's row is
+ *   y = rope(norm(latent[i]), pos[i]) rounded once to bf16, then the csa2_quantize_kv rule
+ * (the sum, the norm, the angle and the products are carried far enough that the rounding
+ * to bf16 is that of the real number), written at position pos[i] of sequence seq[i].
+ * With idx_proj the token's indexer row is its 64 fp32 values, rotated when idx_rope_dim >
+ * 0, in the format of csa2_append_kv.
+ *   - A token with pos < 0 is padding: nothing is written for it.
+ *   - A token whose sequence, position or page lies outside the cache is skipped and, when
+ *     workspace is given, sets CSA2_ERR_DEVICE in its header (csa2_check_device_status).
+ *   - The (seq, pos) of one call must be distinct. */
+typedef struct csa2_append_args {
+    int64_t n;                  /* tokens (>= 0; 0 enqueues nothing)                    */
+    int32_t batch;              /* sequences of the cache, >= 1                         */
+    int32_t rope_dim;           /* rotated channels of the 512: even, 0 .. 512          */
+    int32_t idx_rope_dim;       /* rotated channels of the 64: even, 0 .. 64            */
+    int32_t in_type;            /* CSA2_T_* of latent                                   */
+    int32_t flags;              /* CSA2_ROPE_NORM (latent), CSA2_ROPE_HALF (both)       */
+    float eps;                  /* >= 0                                                 */
+    int64_t latent_stride;      /* elements between tokens; rows 16-byte aligned        */
+    int64_t idx_stride;         /* elements between tokens of idx_proj; rows 8-byte
+                                   aligned                                              */
+    int64_t total_rows;         /* rows of codes / scales (and idx_k / idx_kscale)      */
+    const void* latent;         /* [n][512]                                             */
+    const float* idx_proj;      /* [n][64], or NULL: main rows only                     */
+    const int32_t* seq;         /* [n] sequence of each token, or NULL: token i belongs
+                                   to sequence i (one new token each; n <= batch)       */
+    const int64_t* pos;         /* [n] position in its sequence                         */
+    const int64_t* kv_offsets;  /* [batch+1] packed cache (pos < N_b), or NULL with a
+                                   page table                                           */
+    const int32_t* page_table;  /* [batch][pages_per_seq] as in csa2_layer_args, or NULL */
+    int32_t page_rows;          /* with page_table: rows per page, a multiple of 128    */
+    int32_t pages_per_seq;      /* with page_table                                      */
+    const float* inv_freq;      /* [rope_dim/2] (rope_dim > 0)                          */
+    const float* idx_inv_freq;  /* [idx_rope_dim/2] (idx_rope_dim > 0)                  */
+    const float* weight;        /* [512] (16-byte aligned) or NULL (CSA2_ROPE_NORM only) */
+    uint8_t* codes;             /* [total_rows][256] (8-B aligned)                      */
+    uint8_t* scales;            /* [total_rows][32]                                     */
+    uint8_t* idx_k;             /* with idx_proj: [total_rows][64] (2-B aligned)        */
+    float* idx_kscale;          /* with idx_proj: [total_rows]                          */
+    void* workspace;            /* NULL, or >= 256 bytes, 256-B aligned: the device error
+                                   word of csa2_attend's workspaces                     */
+} csa2_append_args;
+csa2_status csa2_append_rope(const csa2_append_args* a, void* stream);
+
+/* csa2_dequantize_kv — FP4 main-KV rows back to bf16 (exact: a product e2m1 * e4m3 has at
+ * most 6 significant bits).
+ *   codes, scales  the cache (codes 8-B aligned), total_rows rows
+ *   src_row        NULL (rows 0 .. n-1; n <= total_rows) or [n] int64 rows; a row outside
+ *                  [0, total_rows) (the -1 padding of index lists) gives a zero row
+ *   out            [n][512] bf16 (16-B aligned) */
+csa2_status csa2_dequantize_kv(const uint8_t* codes, const uint8_t* scales, int64_t total_rows,
+                               const int64_t* src_row, int64_t n, uint16_t* out, void* stream);
+
+/* csa2_attend_cache — attention of new tokens over the FP4 cache without an index: per query
+ * and head h,
+ *   out_h = sum_j softmax_j(sm_scale * q_h . row_j) row_j
+ * over the visible positions j of its sequence.  Query i of sequence b sees
+ *   n_vis = N_b positions (q_pos NULL), or min(N_b, floor((q_pos[b] + i + 1) / ratio)),
+ * and of those j >= n_vis - window or j < sinks when window > 0 (all when window is 0).
+ * A query that sees nothing gets zeros (lse -inf).  Every query streams its own positions:
+ * the call is made for decode steps and for a few drafted tokens.
+ * The logits use the bf16 query written as six base-8 digits of a per-head fixed point
+ * (exact for elements above 2^-7 of the head's largest, else to 2^-16 of it) times the
+ * stored FP4 rows, summed in fp32; P is rounded to f16 (2^-12) for P V, summed in fp32. */
+typedef struct csa2_cache_args {
+    int32_t batch;              /* B >= 1                                               */
+    int32_t q_per_seq;          /* queries per sequence, 1 .. 65536                     */
+    int32_t ratio;              /* 1 or 2 (with q_pos)                                  */
+    int32_t out_type;           /* CSA2_T_BF16 or CSA2_T_F32                            */
+    int64_t max_n;              /* host upper bound on every N_b (>= 1)                 */
+    int64_t total_n;            /* rows of codes / scales (1 .. 2^31-1)                 */
+    int64_t window;             /* 0: every position; else the last `window` ones       */
+    int64_t sinks;              /* with window: first positions that stay visible       */
+    const int64_t* kv_offsets;  /* [B+1]                                                */
+    const int64_t* q_pos;       /* [B] token of each sequence's first query, or NULL    */
+    const uint8_t* codes;       /* main-KV codes (16-B aligned)                         */
+    const uint8_t* scales;      /* main-KV scales (16-B aligned)                        */
+    const uint16_t* q;          /* [B*q_per_seq][16][512] bf16 (16-B aligned)           */
+    float sm_scale;
+    int32_t reserved0;          /* must be 0                                            */
+    void* out;                  /* [B*q_per_seq][16][512] (16-B aligned)                */
+    float* lse;                 /* [B*q_per_seq][16] natural-log sum of exp(logits), to
+                                   join with other attention over other keys, or NULL   */
+    const int32_t* page_table;  /* as in csa2_layer_args, or NULL                       */
+    int32_t page_rows;
+    int32_t pages_per_seq;
+    void* workspace;            /* >= csa2_cache_workspace_size(this), 256-B aligned, its
+                                   first 256 bytes zeroed before first use; not shared by
+                                   calls that may run at the same time                  */
+    size_t workspace_bytes;
+} csa2_cache_args;
+size_t csa2_cache_workspace_size(const csa2_cache_args* a);
+csa2_status csa2_attend_cache(const csa2_cache_args* a, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
