@@ -226,6 +226,20 @@ bool make_idx_k_map(const uint8_t* idx_k, int64_t rows, int box_rows, CUtensorMa
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// TMA map over rows of `width` bytes, boxes of box_rows x box_width.
+bool make_byte_rows_map(const uint8_t* base, int64_t rows, int width, int box_width, int box_rows,
+                        CUtensorMapSwizzle swizzle, CUtensorMap* map) {
+    const EncodeTiledFn enc = encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(width)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_width), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 bool opt_in_smem(const void* kernel, int bytes) {
@@ -711,7 +725,13 @@ csa2_status csa2_attend_cache(const csa2_cache_args* a, void* stream) {
     p.meta = reinterpret_cast<int32_t*>(ws + L.meta);
     p.part = reinterpret_cast<float*>(ws + L.part);
     p.ranges = L.ranges;
-    return launch_attend_cache(p, static_cast<cudaStream_t>(stream));
+    CUtensorMap codes, scales;
+    if (!make_byte_rows_map(a->codes, a->total_n, ROW_CODES, 128, CACHE_TILE, CU_TENSOR_MAP_SWIZZLE_128B, &codes) ||
+        !make_byte_rows_map(a->scales, a->total_n, ROW_SCALES, ROW_SCALES, CACHE_TILE, CU_TENSOR_MAP_SWIZZLE_NONE, &scales)) {
+        std::snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled failed (cache)");
+        return CSA2_ERR_CUDA;
+    }
+    return launch_attend_cache(p, codes, scales, static_cast<cudaStream_t>(stream));
 }
 
 csa2_status csa2_set_wait_limit(void* workspace, uint32_t polls, void* stream) {

@@ -2,6 +2,8 @@
 // attention over the whole cache.
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
 
 namespace csa2 {
@@ -73,6 +75,9 @@ constexpr int CACHE_TILE = 128;                                  // positions pe
 constexpr int CACHE_MAX_RANGES = 148;                            // one CTA per SM
 constexpr int CACHE_PART_FLOATS = 2 * HEADS + HEADS * D;
 int cache_ranges(int64_t rows, int64_t max_n, int64_t window, int64_t sinks);
-csa2_status launch_attend_cache(const CacheParams& p, cudaStream_t stream);
+// Tensor maps over codes as [total_n][256] bytes (boxes of 128 rows x 128 bytes, 128-byte
+// swizzle) and scales as [total_n][32] bytes (boxes of 128 rows, no swizzle).
+csa2_status launch_attend_cache(const CacheParams& p, const CUtensorMap& codes, const CUtensorMap& scales,
+                                cudaStream_t stream);
 
 }  // namespace csa2
