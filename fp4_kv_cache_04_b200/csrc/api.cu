@@ -81,16 +81,16 @@ bool valid_type(int32_t t) { return t == CSA2_T_BF16 || t == CSA2_T_F16 || t == 
 
 // Workspace of csa2_attend_cache: two partials for each range of the tile list.
 struct CacheLayout {
-    int ranges = 1;
+    CachePlan plan;
     size_t meta = 0, part = 0, total = 0;
 };
 
 CacheLayout cache_layout(const csa2_cache_args* a) {
     CacheLayout L;
-    L.ranges = cache_ranges(static_cast<int64_t>(a->batch) * a->q_per_seq, a->max_n, a->window, a->sinks);
+    L.plan = cache_plan(static_cast<int64_t>(a->batch) * a->q_per_seq, a->max_n, a->window, a->sinks);
     L.meta = WS_HEADER;
-    L.part = L.meta + align_up(static_cast<size_t>(L.ranges) * 2 * sizeof(int32_t), 256);
-    L.total = L.part + align_up(static_cast<size_t>(L.ranges) * 2 * CACHE_PART_FLOATS * sizeof(float), 256);
+    L.part = L.meta + align_up(static_cast<size_t>(L.plan.ranges) * 2 * sizeof(int32_t), 256);
+    L.total = L.part + align_up(static_cast<size_t>(L.plan.ranges) * 2 * CACHE_PART_FLOATS * sizeof(float), 256);
     return L;
 }
 
@@ -724,7 +724,8 @@ csa2_status csa2_attend_cache(const csa2_cache_args* a, void* stream) {
     p.err = reinterpret_cast<unsigned*>(ws);
     p.meta = reinterpret_cast<int32_t*>(ws + L.meta);
     p.part = reinterpret_cast<float*>(ws + L.part);
-    p.ranges = L.ranges;
+    p.ranges = L.plan.ranges;
+    p.whole_rows = L.plan.whole_rows;
     CUtensorMap codes, scales;
     if (!make_byte_rows_map(a->codes, a->total_n, ROW_CODES, 128, CACHE_TILE, CU_TENSOR_MAP_SWIZZLE_128B, &codes) ||
         !make_byte_rows_map(a->scales, a->total_n, ROW_SCALES, ROW_SCALES, CACHE_TILE, CU_TENSOR_MAP_SWIZZLE_NONE, &scales)) {

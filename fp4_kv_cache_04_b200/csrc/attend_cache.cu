@@ -26,10 +26,10 @@ struct RowView {
 
 __device__ __forceinline__ RowView row_view(const CacheParams& p, int64_t row) {
     const int64_t b = row / p.q_per_seq;
-    int64_t n = __ldg(p.kv_offsets + b + 1) - __ldg(p.kv_offsets + b);
+    int64_t n = p.kv_offsets[b + 1] - p.kv_offsets[b];
     n = max(static_cast<int64_t>(0), min(n, p.max_n));
     if (p.q_pos) {
-        const int64_t t = __ldg(p.q_pos + b) + row % p.q_per_seq + 1;
+        const int64_t t = p.q_pos[b] + row % p.q_per_seq + 1;
         n = min(n, max(static_cast<int64_t>(0), t / p.ratio));
     }
     RowView v;
@@ -48,54 +48,67 @@ __device__ __forceinline__ bool visible(const CacheParams& p, const RowView& v, 
 }
 
 // This CTA's range of the tile list: the row it starts in, the tile inside that row, and
-// how many tiles follow.  Whole block; red: >= 33 words of shared memory.
+// how many tiles follow.  Whole block.
 struct Range {
     int64_t row;
     int tile;
     int64_t count;
 };
 
+// Sum of v over the block, and the sum of the threads before this one.  red: 32 words.
+template <int THREADS>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t& before, int64_t* red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    int64_t inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) red[warp] = inc;
+    __syncthreads();
+    int64_t all = 0;
+    before = inc - v;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += red[w];
+        all += red[w];
+    }
+    __syncthreads();
+    return all;
+}
+
 template <int THREADS>
 __device__ __forceinline__ Range my_range(const CacheParams& p, int64_t (&red)[34]) {
-    constexpr int WARPS = THREADS / 32;
     const int64_t rows = static_cast<int64_t>(p.batch) * p.q_per_seq;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
-    int64_t sum = 0;
-    for (int64_t r = tid; r < rows; r += THREADS) sum += row_view(p, r).tiles;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) red[warp] = sum;
-    __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) total += red[w];
-    __syncthreads();
+    const int64_t c = blockIdx.x;
+    int64_t before;
+    if (p.whole_rows) {                                     // rows dealt out uncut
+        const int64_t r0 = rows * c / p.ranges, r1 = rows * (c + 1) / p.ranges;
+        int64_t sum = 0;
+        for (int64_t r = r0 + threadIdx.x; r < r1; r += THREADS) sum += row_view(p, r).tiles;
+        return Range{r0, 0, block_scan<THREADS>(sum, before, red)};
+    }
+    // one pass over the rows finds the total, a second one (none for THREADS rows or fewer)
+    // the row in which this range starts
+    int mine = threadIdx.x < rows ? row_view(p, threadIdx.x).tiles : 0;
+    int64_t sum = mine;
+    for (int64_t r = threadIdx.x + THREADS; r < rows; r += THREADS) sum += row_view(p, r).tiles;
+    const int64_t total = block_scan<THREADS>(sum, before, red);
     // with fewer tiles than ranges the first `total` ranges take one each: a cut row's
     // ranges are always consecutive
-    const int64_t c = blockIdx.x, g = min(static_cast<int64_t>(p.ranges), total);
+    const int64_t g = min(static_cast<int64_t>(p.ranges), total);
     if (c >= g) return Range{0, 0, 0};
     const int64_t t0 = total * c / g, t1 = total * (c + 1) / g;
-    Range out{0, 0, t1 - t0};
-    if (tid == 0) red[32] = -1;
+    if (threadIdx.x == 0) red[32] = -1;
     int64_t base = 0;
     for (int64_t r0 = 0; r0 < rows; r0 += THREADS) {
-        const int64_t r = r0 + tid;
-        const int mine = r < rows ? row_view(p, r).tiles : 0;
-        int64_t inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        if (lane == 31) red[warp] = inc;
-        __syncthreads();
-        int64_t before = base, all = 0;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            if (w < warp) before += red[w];
-            all += red[w];
-        }
-        const int64_t first = before + inc - mine;
+        const int64_t r = r0 + threadIdx.x;
+        if (r0 > 0) mine = r < rows ? row_view(p, r).tiles : 0;
+        int64_t first = before, all = total;
+        if (rows > THREADS) all = block_scan<THREADS>(mine, first, red);
+        else __syncthreads();
+        first += base;
         if (mine > 0 && t0 >= first && t0 < first + mine) {
             red[32] = r;
             red[33] = t0 - first;
@@ -103,17 +116,8 @@ __device__ __forceinline__ Range my_range(const CacheParams& p, int64_t (&red)[3
         base += all;
         __syncthreads();
         if (red[32] >= 0) break;
-        __syncthreads();
     }
-    out.row = red[32];
-    out.tile = static_cast<int>(red[33]);
-    return out;
-}
-
-__device__ __forceinline__ void store_out(const CacheParams& p, int64_t row, int h, int c, float v) {
-    const int64_t at = (row * HEADS + h) * D + c;
-    if (p.out_f32) static_cast<float*>(p.out)[at] = v;
-    else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+    return Range{red[32], static_cast<int>(red[33]), t1 - t0};
 }
 
 // Rows that see nothing: zeros, lse -inf.  One warp of each CTA; CTA c looks at rows 32 c ..
@@ -139,8 +143,8 @@ constexpr int AC_PV_WARPS = 8;                     // warps 0-7: P V
 constexpr int AC_SM_WARP = 8;                      // warps 8-11: softmax (TMEM lane quarters 0-3)
 constexpr int AC_TMA_WARP = 12;
 constexpr int AC_MMA_WARP = 13;
-constexpr int AC_SYNC = AC_THREADS - 32;           // every warp but the producer
-constexpr int AC_STAGES = 5;
+constexpr int AC_Q_WARP = 14;                      // warps 14, 15: the next row's query
+constexpr int AC_STAGES = 4;
 constexpr int AC_CODE_BYTES = CACHE_TILE * ROW_CODES;                    // two panels of 16 KB
 constexpr int AC_STAGE_BYTES = AC_CODE_BYTES + CACHE_TILE * ROW_SCALES;  // 36 KB
 constexpr int AC_DIGITS = 6;
@@ -150,31 +154,29 @@ constexpr int AC_P_BYTES = CACHE_TILE * HEADS * 2;
 // tensor memory: two S accumulators, the tile's scales twice, the digits' scales
 constexpr uint32_t AT_COLS = 512, AT_S = 0, AT_S_STEP = 128, AT_SFA = 256, AT_SFB = 320;
 // named barriers
-constexpr int BAR_ROW = 1, BAR_VOTE = 2, BAR_MAX = 3, BAR_PV = 4;
+constexpr int BAR_VOTE = 1, BAR_MAX = 2, BAR_PV = 3;   // BAR_PV + w: warps w and w + 4
 constexpr float AC_GAP = 4.0f;                     // the reference maximum moves by more than 2^4 ...
 constexpr float AC_SHIFT = 11.0f;                  // ... and P is kept times 2^11, at most 2^15 in f16
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 struct alignas(1024) CacheSmem {
     uint8_t stage[AC_STAGES][AC_STAGE_BYTES];
-    union {
-        struct {
-            uint8_t q[2 * AC_QPANEL];              // query digits, K-major SW128 panels
-            uint8_t p[2][AC_P_BYTES];              // P [key][head] f16
-        } a;
-        float4 x[AC_PV_WARPS][8][32];              // O exchanged between the two key halves
-    } u;
+    uint8_t q[2][2 * AC_QPANEL];                   // query digits of two rows, K-major SW128 panels
+    uint8_t p[2][AC_P_BYTES];                      // P [key][head] f16
     uint8_t sf[2][8][512];                         // a tile's scales as 32 x 16 B blocks
-    uint64_t full[AC_STAGES], empty[AC_STAGES], s_full[2], s_empty[2], p_full[2], p_empty[2], drain;
-    float alpha[2][HEADS];
-    float part_m[4][HEADS], l[4][HEADS], m[HEADS], f[HEADS];
+    float4 x[AC_PV_WARPS / 2][8][32];              // O passed between the two key halves
+    // tiles: loaded / read, S written / read, P written / read; rows: query written / read,
+    // statistics written / read
+    uint64_t full[AC_STAGES], empty[AC_STAGES], s_full[2], s_empty[2], p_full[2], p_empty[2];
+    uint64_t q_full[2], q_empty[2], r_full[2], r_empty[2], drain;
+    float f[2][HEADS], l[2][4][HEADS], m[2][HEADS];
+    float alpha[2][HEADS], part_m[4][HEADS];
     int moved[2];
     int issued[AC_STAGES];                         // copies issued into each stage
     uint32_t tmem;
     int64_t red[34];
 };
 static_assert(sizeof(CacheSmem) + 1024 <= 232448, "shared memory of one SM");
-static_assert(sizeof(CacheSmem::u) == 32768, "O exchange over the query digits and P");
 
 // kind::mxf4nvf4, A = B = E2M1, scales E4M3, M = 128 keys, N = 96
 constexpr uint32_t AC_IDESC = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(AC_N >> 3) << 17) |
@@ -229,15 +231,22 @@ __device__ __forceinline__ int64_t next_row(const CacheParams& p, int64_t row) {
     return rows - 1;
 }
 
-// Head h of the row's query as six balanced base-8 digits: n = rint(q 2^k), 2^15 <= |n| <
+// Head h of a row's query as six balanced base-8 digits: n = rint(q 2^k), 2^15 <= |n| <
 // 2^16 for the head's largest element, n = sum_d e_d 8^d with e_d in -4 .. 3, every one of
 // which E2M1 holds.  Adding 4 to every digit (0o444444) makes them plain octal digits.
 // One warp, lane l holds channels 16 l .. + 15.
-__device__ __forceinline__ void put_query(const CacheParams& p, CacheSmem& sm, int64_t row, int h) {
+struct QueryHead {
+    uint4 a, b;
+};
+
+__device__ __forceinline__ QueryHead load_query(const CacheParams& p, int64_t row, int h) {
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + (row * HEADS + h) * D + (threadIdx.x & 31) * GROUP);
+    return QueryHead{src[0], src[1]};
+}
+
+__device__ __forceinline__ void put_query(const CacheParams& p, CacheSmem& sm, int qb, int h, const QueryHead& v) {
     const int lane = threadIdx.x & 31;
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + (row * HEADS + h) * D + lane * GROUP);
-    const uint4 v0 = __ldg(src), v1 = __ldg(src + 1);
-    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
     uint32_t top = 0;                                       // largest magnitude, as bf16 bits
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
@@ -251,26 +260,60 @@ __device__ __forceinline__ void put_query(const CacheParams& p, CacheSmem& sm, i
         n[2 * i] = static_cast<uint32_t>(__float2int_rn(__uint_as_float(w[i] << 16) * up) + 0x24924);
         n[2 * i + 1] = static_cast<uint32_t>(__float2int_rn(__uint_as_float(w[i] & 0xFFFF0000u) * up) + 0x24924);
     }
-    uint8_t* base = sm.u.a.q + (lane >> 4) * AC_QPANEL + (lane & 1) * 8;
-    const int chunk = (lane & 15) >> 1;
-#pragma unroll
-    for (int d = 0; d < AC_DIGITS; ++d) {
+    uint8_t* base = sm.q[qb] + (lane >> 4) * AC_QPANEL + h * 128 + ((((lane & 15) >> 1) ^ (h & 7)) << 4) + (lane & 1) * 8;
+#pragma unroll 1
+    for (int d = 0; d < AC_DIGITS; ++d) {                   // row 16 d + h
         uint32_t out[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {                       // channels 8 j .. + 7: 4 bytes
             uint32_t even = 0, odd = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                even |= ((n[8 * j + 2 * i] >> (3 * d)) & 7u) << (4 * i);
-                odd |= ((n[8 * j + 2 * i + 1] >> (3 * d)) & 7u) << (4 * i);
+                even |= (n[8 * j + 2 * i] & 7u) << (4 * i);
+                odd |= (n[8 * j + 2 * i + 1] & 7u) << (4 * i);
             }
             // E2M1 codes of -4 .. 3 looked up four at a time
             out[j] = __byte_perm(0x0A0C0D0Eu, 0x05040200u, even) | (__byte_perm(0x0A0C0D0Eu, 0x05040200u, odd) << 4);
         }
-        const int r = d * HEADS + h;
-        *reinterpret_cast<uint2*>(base + r * 128 + ((chunk ^ (r & 7)) << 4)) = make_uint2(out[0], out[1]);
+        *reinterpret_cast<uint2*>(base + d * HEADS * 128) = make_uint2(out[0], out[1]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) n[i] >>= 3;
     }
-    if (lane == 0) sm.f[h] = p.sm_scale * LOG2E * __uint_as_float(static_cast<uint32_t>(9 - k + 127) << 23);
+    if (lane == 0) sm.f[qb][h] = p.sm_scale * LOG2E * __uint_as_float(static_cast<uint32_t>(9 - k + 127) << 23);
+}
+
+// Cache row of position pos of sequence b (RowMap::row with a plain load: the page table may
+// have been written by the kernel this one was launched behind).
+__device__ __forceinline__ int64_t cache_row(const CacheParams& p, int64_t b, int64_t off, int64_t pos) {
+    if (p.rows.page_table == nullptr) return off + pos;
+    return static_cast<int64_t>(p.rows.page_table[b * p.rows.pages_per_seq + pos / p.rows.page_rows]) * p.rows.page_rows +
+           pos % p.rows.page_rows;
+}
+
+// Per-head results of 32 lanes x 16 heads: each step halves the heads a lane still holds,
+// so 16 shuffles do the work of 80.  Lane 2 i (and 2 i + 1) ends with head head_of(lane).
+__device__ __forceinline__ int head_of(int lane) {
+    return ((lane >> 4) & 1) * 8 + ((lane >> 3) & 1) * 4 + ((lane >> 2) & 1) * 2 + ((lane >> 1) & 1);
+}
+
+template <bool MAX>
+__device__ __forceinline__ float reduce_heads(const float (&v)[HEADS]) {
+    const int lane = threadIdx.x & 31;
+    float a[HEADS];
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) a[i] = v[i];
+#pragma unroll
+    for (int n = 8; n >= 1; n /= 2) {
+        const bool up = lane & (2 * n);
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, up ? a[i] : a[n + i], 2 * n);
+            const float mine = up ? a[n + i] : a[i];
+            a[i] = MAX ? fmaxf(mine, got) : mine + got;
+        }
+    }
+    const float got = __shfl_xor_sync(0xFFFFFFFFu, a[0], 1);
+    return MAX ? fmaxf(a[0], got) : a[0] + got;
 }
 
 __global__ void __launch_bounds__(AC_THREADS, 1)
@@ -284,15 +327,19 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
         for (int i = 0; i < AC_STAGES; ++i) {
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], AC_PV_WARPS);
+            sm.issued[i] = 0;
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.s_empty[i], 4);
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.p_empty[i], AC_PV_WARPS);
+            mbar_init(&sm.q_full[i], 2);
+            mbar_init(&sm.q_empty[i], 5);                   // the row's last MMA and the softmax warps
+            mbar_init(&sm.r_full[i], 4);
+            mbar_init(&sm.r_empty[i], AC_PV_WARPS);
         }
         mbar_init(&sm.drain, 1);
-        for (int i = 0; i < AC_STAGES; ++i) sm.issued[i] = 0;
         mbar_fence_init();
     }
     if (warp == AC_MMA_WARP) tmem_alloc(&sm.tmem, AT_COLS);
@@ -315,38 +362,43 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
     }
     griddep_launch_dependents();
     griddep_wait();                                         // nothing global is touched before
-    const Range range = my_range<AC_THREADS>(p, sm.red);
-    if (tid < 2) p.meta[2 * blockIdx.x + tid] = -1;
-    __syncthreads();
-    tc_fence_after();
-
     unsigned* err = p.err;
     const uint32_t limit = wait_limit(err);
+    const Range range = my_range<AC_THREADS>(p, sm.red);
+    if (tid < 2) p.meta[2 * blockIdx.x + tid] = -1;
+
     bool dead = false;                                      // a wait ran out: no more waiting, no more issuing
     auto wait = [&](uint64_t* bar, int phase) {
         if (!dead && !mbar_wait(bar, static_cast<uint32_t>(phase & 1), err, limit)) dead = true;
     };
+    // every role walks the range's rows by itself: it counts tiles, rw rows
+    int it = 0, rw = 0;
+    int64_t row = range.row, left = range.count;
+    int tile = range.tile;
+    if (left > 0) row = next_row(p, row);
 
     if (warp == AC_TMA_WARP) {
         // ---- producer: runs ahead over the rows, AC_STAGES tiles at most
-        int it = 0;
-        int64_t row = range.row, left = range.count;
-        int tile = range.tile;
-        while (left > 0) {
-            row = next_row(p, row);
+        auto load_row = [&](bool first) {
             const RowView v = row_view(p, row);
             const int end = static_cast<int>(min(static_cast<int64_t>(v.tiles), tile + left));
-            const int64_t b = row / p.q_per_seq, off = __ldg(p.kv_offsets + b);
+            const int64_t b = row / p.q_per_seq, off = p.kv_offsets[b];
             for (int t0 = tile; t0 < end; t0 += 32) {
                 int y = 0;                                  // each lane looks one tile's row up
                 if (t0 + lane < end) {
-                    const int64_t r0 = p.rows.row(b, off, v.pos(t0 + lane));
+                    const int64_t r0 = cache_row(p, b, off, v.pos(t0 + lane));
                     const bool bad = r0 < 0 || r0 >= p.total_n;
                     if (bad) atomicOr(err, ERR_DEVICE);
                     y = static_cast<int>(bad ? p.total_n : r0);      // past the end: reads zeros
                 }
                 for (int i = 0; i < 32 && t0 + i < end; ++i, ++it) {
                     const int yi = __shfl_sync(0xFFFFFFFFu, y, i);
+                    // the first row's query is still being written: its barrier comes once the
+                    // ring is full or the row is loaded
+                    if (first && it == AC_STAGES) {
+                        __syncthreads();
+                        first = false;
+                    }
                     if (lane == 0) {
                         const int st = it % AC_STAGES;
                         if (it >= AC_STAGES) wait(&sm.empty[st], it / AC_STAGES - 1);
@@ -362,28 +414,65 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                     __syncwarp();
                 }
             }
+            if (first) __syncthreads();
             left -= end - tile;
             tile = 0;
             ++row;
+        };
+        if (left > 0) load_row(true);
+        else __syncthreads();
+        while (left > 0) {
+            row = next_row(p, row);
+            load_row(false);
         }
         if (lane == 0) {                                    // no copy may land after the CTA is gone
             for (int st = 0; st < AC_STAGES; ++st)
                 if (sm.issued[st]) mbar_wait(&sm.full[st], static_cast<uint32_t>((sm.issued[st] - 1) & 1), err);
         }
     } else {
-        if (warp == AC_WARPS - 1) empty_rows(p);
-        int it = 0;
-        int64_t row = range.row, left = range.count;
-        int tile = range.tile;
-        while (left > 0) {
-            row = next_row(p, row);
-            const RowView v = row_view(p, row);
-            const int end = static_cast<int>(min(static_cast<int64_t>(v.tiles), tile + left));
-            for (int h = warp < AC_TMA_WARP ? warp : warp - 1; h < HEADS; h += AC_WARPS - 1) put_query(p, sm, row, h);
+        // the first row's query: a head per warp; the following rows' by warps 14 and 15
+        if (left > 0) {
+            const int h = warp < AC_TMA_WARP ? warp : warp - 1;
+            put_query(p, sm, 0, h, load_query(p, row, h));
+            if (warp == AC_WARPS - 1) put_query(p, sm, 0, HEADS - 1, load_query(p, row, HEADS - 1));
             fence_proxy_async_smem();
-            named_barrier(BAR_ROW, AC_SYNC);
-
-            if (warp == AC_MMA_WARP) {
+        }
+        __syncthreads();
+        tc_fence_after();
+        if (warp >= AC_Q_WARP) {
+            const int h0 = (warp - AC_Q_WARP) * (HEADS / 2);
+            while (left > 0) {
+                if (rw > 0) {
+                    row = next_row(p, row);
+                    const int qb = rw & 1;
+                    if (rw >= 2) wait(&sm.q_empty[qb], (rw >> 1) - 1);
+#pragma unroll 1
+                    for (int h = 0; h < HEADS / 2; h += 4) {
+                        QueryHead v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = load_query(p, row, h0 + h + i);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) put_query(p, sm, qb, h0 + h + i, v[i]);
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.q_full[rw & 1]);
+                left -= min(static_cast<int64_t>(row_view(p, row).tiles - tile), left);
+                tile = 0;
+                ++row;
+                ++rw;
+            }
+            if (warp == AC_WARPS - 1) empty_rows(p);
+        } else if (warp == AC_MMA_WARP) {
+            const uint64_t dq = umma_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
+            const uint64_t dc = umma_desc_sw128(smem_u32(sm.stage[0]), 16, 1024);
+            const uint64_t ds = desc_rows16(smem_u32(sm.sf[0][0]));
+            while (left > 0) {
+                if (rw > 0) row = next_row(p, row);
+                const int end = static_cast<int>(min(static_cast<int64_t>(row_view(p, row).tiles), tile + left));
+                wait(&sm.q_full[rw & 1], rw >> 1);
+                const uint64_t dqr = dq + (rw & 1) * (2 * AC_QPANEL / 16);
                 for (int t = tile; t < end; ++t, ++it) {
                     const int st = it % AC_STAGES, buf = it & 1;
                     wait(&sm.full[st], it / AC_STAGES);
@@ -405,29 +494,44 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0 && !dead) {
-                        const uint32_t sfa = tm + AT_SFA + 32 * buf;
+                        const uint32_t sfa = tm + AT_SFA + 32 * buf, dst = tm + AT_S + AT_S_STEP * buf;
+                        const uint64_t da = dc + st * (AC_STAGE_BYTES / 16), dsb = ds + buf * (8 * 512 / 16);
 #pragma unroll
-                        for (int s = 0; s < 8; ++s) tmem_copy_rows16(sfa + 4 * s, desc_rows16(smem_u32(sm.sf[buf][s])));
-                        const uint32_t ca = smem_u32(sm.stage[st]), qa = smem_u32(sm.u.a.q);
+                        for (int s = 0; s < 8; ++s) tmem_copy_rows16(sfa + 4 * s, dsb + s * (512 / 16));
 #pragma unroll
-                        for (int s = 0; s < 8; ++s) {
-                            const uint64_t da = umma_desc_sw128(ca + (s >> 2) * (AC_CODE_BYTES / 2) + (s & 3) * 32, 16, 1024);
-                            const uint64_t db = umma_desc_sw128(qa + (s >> 2) * AC_QPANEL + (s & 3) * 32, 16, 1024);
-                            mma_nvf4(tm + AT_S + AT_S_STEP * buf, da, db, AC_IDESC, sfa + 4 * s, tm + AT_SFB + 4 * s, s > 0);
-                        }
+                        for (int s = 0; s < 8; ++s)
+                            mma_nvf4(dst, da + (s >> 2) * (AC_CODE_BYTES / 2 / 16) + (s & 3) * 2,
+                                     dqr + (s >> 2) * (AC_QPANEL / 16) + (s & 3) * 2, AC_IDESC, sfa + 4 * s,
+                                     tm + AT_SFB + 4 * s, s > 0);
                         mma_commit(&sm.s_full[buf]);
+                        if (t + 1 == end) mma_commit(&sm.q_empty[rw & 1]);
                     }
                     __syncwarp();
                 }
-            } else if (warp >= AC_SM_WARP && warp < AC_SM_WARP + 4) {
-                // ---- softmax: thread = key
-                const int quarter = warp & 3, key = 32 * quarter + lane;
+                left -= end - tile;
+                tile = 0;
+                ++row;
+                ++rw;
+            }
+            if (lane == 0) {
+                mma_commit(&sm.drain);
+                mbar_wait(&sm.drain, 0, err);
+            }
+        } else if (warp >= AC_SM_WARP) {
+            // ---- softmax: thread = key
+            const int quarter = warp & 3, key = 32 * quarter + lane;
+            while (left > 0) {
+                if (rw > 0) row = next_row(p, row);
+                const RowView v = row_view(p, row);
+                const int end = static_cast<int>(min(static_cast<int64_t>(v.tiles), tile + left));
+                const int rb = rw & 1;
                 float m[HEADS], l[HEADS];
 #pragma unroll
                 for (int h = 0; h < HEADS; ++h) {
                     m[h] = -INFINITY;
                     l[h] = 0.0f;
                 }
+                wait(&sm.q_full[rb], rw >> 1);               // f
                 for (int t = tile; t < end; ++t, ++it) {
                     const int st = it % AC_STAGES, buf = it & 1;
                     const bool vis = visible(p, v, v.pos(t) + key);
@@ -451,19 +555,14 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                     float d = -INFINITY;
 #pragma unroll
                     for (int h = 0; h < HEADS; ++h) {
-                        s[h] = vis ? s[h] * sm.f[h] : -INFINITY;
+                        s[h] = vis ? s[h] * sm.f[rb][h] : -INFINITY;
                         d = fmaxf(d, s[h] - m[h]);           // (-inf) - (-inf): NaN, which fmaxf drops
                     }
                     if (it >= 2) wait(&sm.p_empty[buf], (it >> 1) - 1);
                     const bool moved = vote_barrier(BAR_VOTE, 128, d > AC_GAP);
                     if (moved) {
-#pragma unroll
-                        for (int h = 0; h < HEADS; ++h) {
-                            float x = s[h];
-#pragma unroll
-                            for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
-                            if (lane == 0) sm.part_m[quarter][h] = x;
-                        }
+                        const float top = reduce_heads<true>(s);
+                        if (!(lane & 1)) sm.part_m[quarter][head_of(lane)] = top;
                         named_barrier(BAR_MAX, 128);
 #pragma unroll
                         for (int h = 0; h < HEADS; ++h) {
@@ -486,7 +585,7 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         const __half2 two = __floats2half2_rn(a, b);
                         pk[h / 2] = *reinterpret_cast<const uint32_t*>(&two);
                     }
-                    uint8_t* dst = sm.u.a.p[buf] + key * 32;
+                    uint8_t* dst = sm.p[buf] + key * 32;
                     const int x = ((key >> 2) & 1) << 4;
                     *reinterpret_cast<uint4*>(dst + x) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     *reinterpret_cast<uint4*>(dst + (x ^ 16)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
@@ -500,25 +599,35 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.p_full[buf]);
                 }
+                if (rw >= 2) wait(&sm.r_empty[rb], (rw >> 1) - 1);
+                const float sum = reduce_heads<false>(l);
+                if (!(lane & 1)) sm.l[rb][quarter][head_of(lane)] = sum;
+                if (tid == 32 * AC_SM_WARP) {
 #pragma unroll
-                for (int h = 0; h < HEADS; ++h) {
-                    float x = l[h];
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-                    if (lane == 0) {
-                        sm.l[quarter][h] = x;
-                        if (quarter == 0) sm.m[h] = m[h];
-                    }
+                    for (int h = 0; h < HEADS; ++h) sm.m[rb][h] = m[h];
                 }
-                named_barrier(BAR_ROW, AC_SYNC);
-            } else if (warp < AC_PV_WARPS) {
-                // ---- P V: warp owns channels 128 (w % 4) .. + 127 of keys 64 (w / 4) .. + 63; lane
-                // (g, t) converts channels 16 g .. + 15 of those (one scale group) of the keys of its
-                // B fragments, n-tile i being channel i of every group
-                const int wq = warp & 3, kh = warp >> 2, g = lane >> 2, t4 = lane & 3;
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm.r_full[rb]);
+                    mbar_arrive(&sm.q_empty[rb]);
+                }
+                left -= end - tile;
+                tile = 0;
+                ++row;
+                ++rw;
+            }
+        } else {
+            // ---- P V: warp owns channels 128 (w % 4) .. + 127 of keys 64 (w / 4) .. + 63; lane
+            // (g, t) converts channels 16 g .. + 15 of those (one scale group) of the keys of its
+            // B fragments, n-tile i being channel i of every group
+            const int wq = warp & 3, kh = warp >> 2, g = lane >> 2, t4 = lane & 3;
+            const uint32_t code_off = (wq >> 1) * (AC_CODE_BYTES / 2) + (g & 1) * 8;
+            const uint32_t chunk = (wq & 1) * 4 + (g >> 1);
+            while (left > 0) {
+                if (rw > 0) row = next_row(p, row);
+                const int tiles = row_view(p, row).tiles;
+                const int end = static_cast<int>(min(static_cast<int64_t>(tiles), tile + left));
                 float o[16][4] = {};
-                const uint32_t code_off = (wq >> 1) * (AC_CODE_BYTES / 2) + (g & 1) * 8;
-                const uint32_t chunk = (wq & 1) * 4 + (g >> 1);
                 for (int t = tile; t < end; ++t, ++it) {
                     const int st = it % AC_STAGES, buf = it & 1;
                     wait(&sm.full[st], it / AC_STAGES);
@@ -535,8 +644,8 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                     }
                     const uint8_t* codes = sm.stage[st] + code_off;
                     const uint8_t* scales = sm.stage[st] + AC_CODE_BYTES + wq * 8 + g;
-                    const uint32_t pa = smem_u32(sm.u.a.p[buf]);
-#pragma unroll
+                    const uint32_t pa = smem_u32(sm.p[buf]);
+#pragma unroll 2
                     for (int ks = 0; ks < 4; ++ks) {
                         const int kb = 64 * kh + 16 * ks;
                         uint32_t a[4];
@@ -577,38 +686,45 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         mbar_arrive(&sm.empty[st]);
                     }
                 }
-                named_barrier(BAR_ROW, AC_SYNC);            // every MMA of the row has read its operands
-                // ---- the two key halves swap half of their channels: warp finishes n-tiles 8 kh .. + 7
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float (&mine)[4] = kh ? o[i] : o[8 + i];
-                    sm.u.x[warp][i][lane] = make_float4(mine[0], mine[1], mine[2], mine[3]);
-                }
-                named_barrier(BAR_PV, 32 * AC_PV_WARPS);
-                const bool whole = tile == 0 && end == v.tiles;
+                // ---- the key halves: warps 4-7 hand n-tiles 0 .. 7 over and take 8 .. 15
+                const bool whole = tile == 0 && end == tiles;
                 const int slot = 2 * blockIdx.x + (tile == 0 ? 1 : 0);     // 0: the row this range starts in
                 float* part = p.part + static_cast<int64_t>(slot) * CACHE_PART_FLOATS;
-                float r[8][4];
+                const int rb = rw & 1;
+                if (kh) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 other = sm.u.x[warp ^ 4][i][lane];
-                    const float (&mine)[4] = kh ? o[8 + i] : o[i];
-                    r[i][0] = mine[0] + other.x;
-                    r[i][1] = mine[1] + other.y;
-                    r[i][2] = mine[2] + other.z;
-                    r[i][3] = mine[3] + other.w;
+                    for (int i = 0; i < 8; ++i) sm.x[wq][i][lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
                 }
+                named_barrier(BAR_PV + wq, 64);
+                if (!kh) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 u = sm.x[wq][i][lane];
+                        o[i][0] += u.x, o[i][1] += u.y, o[i][2] += u.z, o[i][3] += u.w;
+                        sm.x[wq][i][lane] = make_float4(o[8 + i][0], o[8 + i][1], o[8 + i][2], o[8 + i][3]);
+                    }
+                }
+                named_barrier(BAR_PV + wq, 64);
+                if (kh) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 u = sm.x[wq][i][lane];
+                        o[i][0] = o[8 + i][0] + u.x, o[i][1] = o[8 + i][1] + u.y;
+                        o[i][2] = o[8 + i][2] + u.z, o[i][3] = o[8 + i][3] + u.w;
+                    }
+                }
+                wait(&sm.r_full[rb], rw >> 1);
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     const int h = g + 8 * hh;
-                    const float ls = sm.l[0][h] + sm.l[1][h] + sm.l[2][h] + sm.l[3][h];
+                    const float ls = sm.l[rb][0][h] + sm.l[rb][1][h] + sm.l[rb][2][h] + sm.l[rb][3][h];
                     const float inv = whole ? 1.0f / ls : 1.0f;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int ch = 128 * wq + 16 * (2 * t4 + e) + 8 * kh;
                         float val[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) val[i] = r[i][2 * hh + e] * inv;
+                        for (int i = 0; i < 8; ++i) val[i] = o[i][2 * hh + e] * inv;
                         const int64_t at = (row * HEADS + h) * D + ch;
                         if (whole && !p.out_f32) {
                             uint32_t w[4];
@@ -625,29 +741,23 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                             dst[1] = make_float4(val[4], val[5], val[6], val[7]);
                         }
                     }
-                    if (wq == 0 && kh == 0 && t4 == 0) {
+                    if (warp == 0 && t4 == 0) {
                         if (!whole) {
-                            part[h] = sm.m[h] - AC_SHIFT;
+                            part[h] = sm.m[rb][h] - AC_SHIFT;
                             part[HEADS + h] = ls;
                         } else if (p.lse) {
-                            p.lse[row * HEADS + h] = (sm.m[h] - AC_SHIFT + log2f(ls)) * LN2;
+                            p.lse[row * HEADS + h] = (sm.m[rb][h] - AC_SHIFT + log2f(ls)) * LN2;
                         }
                     }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.r_empty[rb]);
                 if (!whole && tid == 0) p.meta[slot] = static_cast<int32_t>(row);
+                left -= end - tile;
+                tile = 0;
+                ++row;
+                ++rw;
             }
-            if (warp >= AC_MMA_WARP) {
-                it += warp == AC_MMA_WARP ? 0 : end - tile;
-                named_barrier(BAR_ROW, AC_SYNC);
-            }
-            named_barrier(BAR_ROW, AC_SYNC);                // the exchange is read: the next query may be written
-            left -= end - tile;
-            tile = 0;
-            ++row;
-        }
-        if (warp == AC_MMA_WARP && lane == 0) {
-            mma_commit(&sm.drain);
-            mbar_wait(&sm.drain, 0, err);
         }
     }
     tc_fence_before();
@@ -658,75 +768,103 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
 
 // Joins the partials of one cut row.  Block (x, y): the x-th cut row (the x-th range whose
 // first partial is its row's last one), 512 / AJ_SLICES channels.  A row's partials are
-// partial 1 of the range it starts in and partials 0 of the following ones, in that order.
+// partial 1 of the range it starts in and
+// partials 0 of the following ones, in that order: four groups of threads take every fourth
+// and are added up in group order.
 constexpr int AJ_SLICES = 16;
-constexpr int AJ_THREADS = 128;
+constexpr int AJ_GROUPS = 4;
+constexpr int AJ_THREADS = 128 * AJ_GROUPS;
 
 __global__ void __launch_bounds__(AJ_THREADS)
 join_cache_kernel(CacheParams p) {
-    __shared__ int sh[2];
     __shared__ int32_t meta[2 * CACHE_MAX_RANGES];
-    const int tid = threadIdx.x;
+    __shared__ float w[CACHE_MAX_RANGES][HEADS], lw[CACHE_MAX_RANGES][HEADS];
+    __shared__ int sh_first, sh_last;
+    __shared__ float4 acc[AJ_GROUPS - 1][128];
+    const int tid = threadIdx.x, lane = tid & 31;
     griddep_wait();
-    for (int i = tid; i < 2 * p.ranges; i += AJ_THREADS) meta[i] = p.meta[i];
+    for (int i = tid; i < 2 * p.ranges; i += AJ_THREADS) meta[i] = __ldcg(p.meta + i);
+    if (tid == 0) sh_last = -1;
     __syncthreads();
-    if (tid == 0) {
-        int seen = 0, last = -1;
-        for (int g = 0; g < p.ranges; ++g) {
-            const int32_t r = meta[2 * g];
-            if (r < 0 || (g + 1 < p.ranges && meta[2 * (g + 1)] == r)) continue;
-            if (seen++ == static_cast<int>(blockIdx.x)) {
-                last = g;
-                break;
+    if (tid < 32) {
+        int seen = 0, last = -1, first = -1;
+        for (int g0 = 0; g0 < p.ranges && last < 0; g0 += 32) {
+            const int g = g0 + lane;
+            const bool end = g < p.ranges && meta[2 * g] >= 0 && (g + 1 >= p.ranges || meta[2 * g + 2] != meta[2 * g]);
+            unsigned any = __ballot_sync(0xFFFFFFFFu, end);
+            for (; any && last < 0; any &= any - 1)
+                if (seen++ == static_cast<int>(blockIdx.x)) last = g0 + __ffs(any) - 1;
+        }
+        if (last >= 0) {                                    // the range whose second partial is this row's
+            for (int g0 = last; first < 0; g0 -= 32) {
+                const int g = g0 - lane;
+                const unsigned any = __ballot_sync(0xFFFFFFFFu, g <= 0 || meta[2 * g + 1] == meta[2 * last]);
+                if (any) first = max(0, g0 - (__ffs(any) - 1));
             }
         }
-        int first = last;
-        if (last >= 0) {
-            const int32_t r = meta[2 * last];
-            while (first > 0 && meta[2 * first + 1] != r) --first;
+        if (lane == 0) {
+            sh_first = first;
+            sh_last = last;
         }
-        sh[0] = first;
-        sh[1] = last;
     }
     __syncthreads();
-    const int first = sh[0], last = sh[1];
+    const int first = sh_first, last = sh_last, n = last - first + 1;
     if (last < 0) return;
+    auto part = [&](int i) { return p.part + static_cast<int64_t>(2 * (first + i) + (i == 0 ? 1 : 0)) * CACHE_PART_FLOATS; };
+    for (int i = tid; i < n * HEADS; i += AJ_THREADS) {
+        w[i / HEADS][i % HEADS] = __ldcg(part(i / HEADS) + i % HEADS);
+        lw[i / HEADS][i % HEADS] = __ldcg(part(i / HEADS) + HEADS + i % HEADS);
+    }
+    __syncthreads();
     const int64_t row = meta[2 * last];
-    const int h = tid / 8, c = blockIdx.y * (D / AJ_SLICES) + (tid % 8) * 4;
-    float m = -INFINITY;
-    for (int g = first; g <= last; ++g)
-        m = fmaxf(m, p.part[static_cast<int64_t>(2 * g + (g == first ? 1 : 0)) * CACHE_PART_FLOATS + h]);
-    float l = 0.0f;
+    const int grp = tid / 128, h = (tid % 128) / 8, c = blockIdx.y * (D / AJ_SLICES) + (tid % 8) * 4;
+    float m = -INFINITY, l = 0.0f;
+    for (int i = 0; i < n; ++i) m = fmaxf(m, w[i][h]);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int g = first; g <= last; ++g) {
-        const float* part = p.part + static_cast<int64_t>(2 * g + (g == first ? 1 : 0)) * CACHE_PART_FLOATS;
-        const float a = part[h] == -INFINITY ? 0.0f : exp2f(part[h] - m);
-        const float4 v = *reinterpret_cast<const float4*>(part + 2 * HEADS + h * D + c);
-        l = fmaf(a, part[HEADS + h], l);
+#pragma unroll 4
+    for (int i = grp; i < n; i += AJ_GROUPS) {
+        const float a = fast_exp2(w[i][h] - m);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(part(i) + 2 * HEADS + h * D + c));
         o.x = fmaf(a, v.x, o.x);
         o.y = fmaf(a, v.y, o.y);
         o.z = fmaf(a, v.z, o.z);
         o.w = fmaf(a, v.w, o.w);
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    store_out(p, row, h, c, o.x * inv);
-    store_out(p, row, h, c + 1, o.y * inv);
-    store_out(p, row, h, c + 2, o.z * inv);
-    store_out(p, row, h, c + 3, o.w * inv);
-    if (p.lse && blockIdx.y == 0 && tid % 8 == 0) p.lse[row * HEADS + h] = (m + log2f(l)) * 0.6931471805599453f;
+    if (grp) acc[grp - 1][tid % 128] = o;
+    __syncthreads();
+    if (grp) return;
+    for (int i = 0; i < n; ++i) l = fmaf(fast_exp2(w[i][h] - m), lw[i][h], l);
+#pragma unroll
+    for (int i = 0; i < AJ_GROUPS - 1; ++i) {
+        const float4 v = acc[i][tid];
+        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    }
+    const float inv = 1.0f / l;
+    const int64_t at = (row * HEADS + h) * D + c;
+    if (p.out_f32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+    if (p.lse && blockIdx.y == 0 && tid % 8 == 0) p.lse[row * HEADS + h] = (m + log2f(l)) * LN2;
 }
 
 }  // namespace
 
-int cache_ranges(int64_t rows, int64_t max_n, int64_t window, int64_t sinks) {
+CachePlan cache_plan(int64_t rows, int64_t max_n, int64_t window, int64_t sinks) {
     // tiles of a row at most: the window may straddle one tile more than its length
     int64_t tiles = ceil_div(max_n, CACHE_TILE);
     if (window > 0) {
         const int64_t w = std::min(window, max_n), s = std::min(sinks, max_n);
         tiles = std::min(tiles, ceil_div(w, CACHE_TILE) + 1 + ceil_div(s, CACHE_TILE));
     }
-    if (rows >= CACHE_MAX_RANGES || tiles >= CACHE_MAX_RANGES) return CACHE_MAX_RANGES;
-    return static_cast<int>(std::min<int64_t>(CACHE_MAX_RANGES, std::max<int64_t>(1, rows * tiles)));
+    CachePlan plan;
+    plan.whole_rows = tiles <= CACHE_UNCUT_TILES;
+    const int64_t most = plan.whole_rows ? rows : tiles >= CACHE_MAX_RANGES ? tiles : rows * tiles;
+    plan.ranges = static_cast<int>(std::min<int64_t>(CACHE_MAX_RANGES, most));
+    return plan;
 }
 
 csa2_status launch_attend_cache(const CacheParams& p, const CUtensorMap& codes, const CUtensorMap& scales,
@@ -746,7 +884,7 @@ csa2_status launch_attend_cache(const CacheParams& p, const CUtensorMap& codes, 
     cfg.numAttrs = 1;
     cudaLaunchKernelEx(&cfg, attend_cache_kernel, p, codes, scales);
     csa2_status st = check_launch("attend_cache_kernel");
-    if (st != CSA2_OK || p.ranges == 1) return st;
+    if (st != CSA2_OK || p.ranges == 1 || p.whole_rows) return st;
     const int64_t rows = static_cast<int64_t>(p.batch) * p.q_per_seq;
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(rows, p.ranges - 1)), AJ_SLICES);
     cfg.blockDim = dim3(AJ_THREADS);

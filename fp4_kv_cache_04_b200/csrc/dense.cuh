@@ -70,11 +70,17 @@ struct CacheParams {
     int32_t* meta;            // [ranges][2] rows of a range's two partials (-1: none)
     float* part;              // [ranges][2] partials: m[16], l[16], O[16][512]
     int ranges;
+    int whole_rows;           // ranges are whole rows: nothing to join
 };
 constexpr int CACHE_TILE = 128;                                  // positions per tile
 constexpr int CACHE_MAX_RANGES = 148;                            // one CTA per SM
 constexpr int CACHE_PART_FLOATS = 2 * HEADS + HEADS * D;
-int cache_ranges(int64_t rows, int64_t max_n, int64_t window, int64_t sinks);
+constexpr int CACHE_UNCUT_TILES = 4;
+struct CachePlan {
+    int ranges;
+    bool whole_rows;
+};
+CachePlan cache_plan(int64_t rows, int64_t max_n, int64_t window, int64_t sinks);
 // Tensor maps over codes as [total_n][256] bytes (boxes of 128 rows x 128 bytes, 128-byte
 // swizzle) and scales as [total_n][32] bytes (boxes of 128 rows, no swizzle).
 csa2_status launch_attend_cache(const CacheParams& p, const CUtensorMap& codes, const CUtensorMap& scales,
