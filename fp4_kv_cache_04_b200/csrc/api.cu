@@ -691,6 +691,7 @@ csa2_status csa2_attend_cache(const csa2_cache_args* a, void* stream) {
     if (a->reserved0 != 0 || a->max_n < 1 || a->total_n < 1 || a->total_n > INT32_MAX || a->window < 0 || a->sinks < 0)
         return CSA2_ERR_INVALID_ARG;
     if (a->max_n > INT32_MAX || static_cast<int64_t>(a->batch) * a->q_per_seq > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
+    if (ceil_div(a->max_n, CACHE_TILE) * a->batch * a->q_per_seq > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
     if (!a->kv_offsets || !a->codes || !a->scales || !a->q || !a->out) return CSA2_ERR_INVALID_ARG;
     if (!(a->sm_scale - a->sm_scale == 0.0f)) return CSA2_ERR_INVALID_ARG;          // finite
     if (!aligned(a->codes, 16) || !aligned(a->scales, 16) || !aligned(a->q, 16) || !aligned(a->out, 16) ||

@@ -24,12 +24,12 @@ struct RowView {
     __device__ __forceinline__ int pos(int tile) const { return (tile < ts ? tile : w0 + tile - ts) * CACHE_TILE; }
 };
 
-__device__ __forceinline__ RowView row_view(const CacheParams& p, int64_t row) {
-    const int64_t b = row / p.q_per_seq;
+__device__ __forceinline__ RowView row_view(const CacheParams& p, int row) {
+    const int b = row / p.q_per_seq;
     int64_t n = p.kv_offsets[b + 1] - p.kv_offsets[b];
     n = max(static_cast<int64_t>(0), min(n, p.max_n));
     if (p.q_pos) {
-        const int64_t t = p.q_pos[b] + row % p.q_per_seq + 1;
+        const int64_t t = p.q_pos[b] + (row - b * p.q_per_seq) + 1;
         n = min(n, max(static_cast<int64_t>(0), t / p.ratio));
     }
     RowView v;
@@ -50,9 +50,7 @@ __device__ __forceinline__ bool visible(const CacheParams& p, const RowView& v, 
 // This CTA's range of the tile list: the row it starts in, the tile inside that row, and
 // how many tiles follow.  Whole block.
 struct Range {
-    int64_t row;
-    int tile;
-    int64_t count;
+    int row, tile, count;
 };
 
 // Sum of v over the block, and the sum of the threads before this one.  red: 32 words.
@@ -86,14 +84,14 @@ __device__ __forceinline__ Range my_range(const CacheParams& p, int64_t (&red)[3
     if (p.whole_rows) {                                     // rows dealt out uncut
         const int64_t r0 = rows * c / p.ranges, r1 = rows * (c + 1) / p.ranges;
         int64_t sum = 0;
-        for (int64_t r = r0 + threadIdx.x; r < r1; r += THREADS) sum += row_view(p, r).tiles;
-        return Range{r0, 0, block_scan<THREADS>(sum, before, red)};
+        for (int64_t r = r0 + threadIdx.x; r < r1; r += THREADS) sum += row_view(p, static_cast<int>(r)).tiles;
+        return Range{static_cast<int>(r0), 0, static_cast<int>(block_scan<THREADS>(sum, before, red))};
     }
     // one pass over the rows finds the total, a second one (none for THREADS rows or fewer)
     // the row in which this range starts
     int mine = threadIdx.x < rows ? row_view(p, threadIdx.x).tiles : 0;
     int64_t sum = mine;
-    for (int64_t r = threadIdx.x + THREADS; r < rows; r += THREADS) sum += row_view(p, r).tiles;
+    for (int64_t r = threadIdx.x + THREADS; r < rows; r += THREADS) sum += row_view(p, static_cast<int>(r)).tiles;
     const int64_t total = block_scan<THREADS>(sum, before, red);
     // with fewer tiles than ranges the first `total` ranges take one each: a cut row's
     // ranges are always consecutive
@@ -117,7 +115,7 @@ __device__ __forceinline__ Range my_range(const CacheParams& p, int64_t (&red)[3
         __syncthreads();
         if (red[32] >= 0) break;
     }
-    return Range{red[32], static_cast<int>(red[33]), t1 - t0};
+    return Range{static_cast<int>(red[32]), static_cast<int>(red[33]), static_cast<int>(t1 - t0)};
 }
 
 // Rows that see nothing: zeros, lse -inf.  One warp of each CTA; CTA c looks at rows 32 c ..
@@ -126,7 +124,7 @@ __device__ __forceinline__ void empty_rows(const CacheParams& p) {
     const int64_t rows = static_cast<int64_t>(p.batch) * p.q_per_seq;
     const int lane = threadIdx.x & 31;
     for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32; r0 < rows; r0 += static_cast<int64_t>(gridDim.x) * 32) {
-        unsigned none = __ballot_sync(0xFFFFFFFFu, r0 + lane < rows && row_view(p, r0 + lane).tiles == 0);
+        unsigned none = __ballot_sync(0xFFFFFFFFu, r0 + lane < rows && row_view(p, static_cast<int>(r0) + lane).tiles == 0);
         for (; none; none &= none - 1) {
             const int64_t r = r0 + __ffs(none) - 1;
             uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + r * HEADS * D * (p.out_f32 ? 4 : 2));
@@ -137,13 +135,12 @@ __device__ __forceinline__ void empty_rows(const CacheParams& p) {
 }
 
 // ---------------------------------------------------------------- the kernel
-constexpr int AC_THREADS = 512;
-constexpr int AC_WARPS = AC_THREADS / 32;
-constexpr int AC_PV_WARPS = 8;                     // warps 0-7: P V
-constexpr int AC_SM_WARP = 8;                      // warps 8-11: softmax (TMEM lane quarters 0-3)
-constexpr int AC_TMA_WARP = 12;
-constexpr int AC_MMA_WARP = 13;
-constexpr int AC_Q_WARP = 14;                      // warps 14, 15: the next row's query
+constexpr int AC_THREADS = 736;
+constexpr int AC_PV_WARPS = 16;                    // warps 0-7, 8-15: P V of a tile's first / last 64 keys
+constexpr int AC_SM_WARP = 16;                     // warps 16-19: softmax (TMEM lane quarters 0-3)
+constexpr int AC_TMA_WARP = 20;
+constexpr int AC_MMA_WARP = 21;                    // warps 21, 22: scales and MMAs of even / odd tiles,
+                                                   // and half of the next row's query each
 constexpr int AC_STAGES = 4;
 constexpr int AC_CODE_BYTES = CACHE_TILE * ROW_CODES;                    // two panels of 16 KB
 constexpr int AC_STAGE_BYTES = AC_CODE_BYTES + CACHE_TILE * ROW_SCALES;  // 36 KB
@@ -154,7 +151,7 @@ constexpr int AC_P_BYTES = CACHE_TILE * HEADS * 2;
 // tensor memory: two S accumulators, the tile's scales twice, the digits' scales
 constexpr uint32_t AT_COLS = 512, AT_S = 0, AT_S_STEP = 128, AT_SFA = 256, AT_SFB = 320;
 // named barriers
-constexpr int BAR_VOTE = 1, BAR_MAX = 2, BAR_PV = 3;   // BAR_PV + w: warps w and w + 4
+constexpr int BAR_VOTE = 1, BAR_MAX = 2, BAR_PV = 3;   // BAR_PV + w: warps w and w + 8
 constexpr float AC_GAP = 4.0f;                     // the reference maximum moves by more than 2^4 ...
 constexpr float AC_SHIFT = 11.0f;                  // ... and P is kept times 2^11, at most 2^15 in f16
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
@@ -164,14 +161,15 @@ struct alignas(1024) CacheSmem {
     uint8_t q[2][2 * AC_QPANEL];                   // query digits of two rows, K-major SW128 panels
     uint8_t p[2][AC_P_BYTES];                      // P [key][head] f16
     uint8_t sf[2][8][512];                         // a tile's scales as 32 x 16 B blocks
-    float4 x[AC_PV_WARPS / 2][8][32];              // O passed between the two key halves
+    float4 x[AC_PV_WARPS / 2][4][32];              // O passed between the two key halves
     // tiles: loaded / read, S written / read, P written / read; rows: query written / read,
     // statistics written / read
     uint64_t full[AC_STAGES], empty[AC_STAGES], s_full[2], s_empty[2], p_full[2], p_empty[2];
     uint64_t q_full[2], q_empty[2], r_full[2], r_empty[2], drain;
-    float f[2][HEADS], l[2][4][HEADS], m[2][HEADS];
-    float alpha[2][HEADS], part_m[4][HEADS];
-    int moved[2];
+    // per row: logit factors, sums, minus the reference maxima (less AC_SHIFT: P = exp2(logit - m));
+    // per tile: the reference its P stands at
+    alignas(16) float f[2][HEADS], l[2][4][HEADS], minus_m[2][HEADS];
+    alignas(16) float ref[2][HEADS], part_m[4][HEADS];
     int issued[AC_STAGES];                         // copies issued into each stage
     uint32_t tmem;
     int64_t red[34];
@@ -220,13 +218,56 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
+// TMA box load of a stream that is read once: its lines leave L2 first, so that code, queries
+// and partials stay.
+__device__ __forceinline__ void tma_load_stream(void* smem_dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
+                                                uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], "
+        "[%4], %5;"
+        :: "r"(smem_u32(smem_dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy) : "memory");
+}
+
+// Two floats in one register pair, for the packed fp32 instructions.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// x[h] = s[h] f[h] + c[h] for the 16 heads, packed; f and c in shared memory.
+__device__ __forceinline__ void scale_heads(const uint64_t (&s)[HEADS / 2], const float* f, const float* c, float (&x)[HEADS]) {
+#pragma unroll
+    for (int i = 0; i < HEADS / 4; ++i) {
+        const ulonglong2 fv = *reinterpret_cast<const ulonglong2*>(f + 4 * i), cv = *reinterpret_cast<const ulonglong2*>(c + 4 * i);
+        const float2 a = unpack2(fma2(s[2 * i], fv.x, cv.x)), b = unpack2(fma2(s[2 * i + 1], fv.y, cv.y));
+        x[4 * i] = a.x, x[4 * i + 1] = a.y, x[4 * i + 2] = b.x, x[4 * i + 3] = b.y;
+    }
+}
+
 // Next row at or after `row` that sees anything (whole warp; there is one).
-__device__ __forceinline__ int64_t next_row(const CacheParams& p, int64_t row) {
-    const int64_t rows = static_cast<int64_t>(p.batch) * p.q_per_seq;
+__device__ __forceinline__ int next_row(const CacheParams& p, int row) {
+    const int rows = p.batch * p.q_per_seq;
     for (; row < rows; row += 32) {
-        const int64_t r = row + (threadIdx.x & 31);
-        const unsigned any = __ballot_sync(0xFFFFFFFFu, r < rows && row_view(p, r).tiles > 0);
+        const int r = row + (threadIdx.x & 31);
+        const unsigned any = __ballot_sync(0xFFFFFFFFu, r < rows && r >= row && row_view(p, r).tiles > 0);
         if (any) return row + __ffs(any) - 1;
+        if (row > rows - 32) break;
     }
     return rows - 1;
 }
@@ -239,8 +280,8 @@ struct QueryHead {
     uint4 a, b;
 };
 
-__device__ __forceinline__ QueryHead load_query(const CacheParams& p, int64_t row, int h) {
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + (row * HEADS + h) * D + (threadIdx.x & 31) * GROUP);
+__device__ __forceinline__ QueryHead load_query(const CacheParams& p, int row, int h) {
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(row) * HEADS + h) * D + (threadIdx.x & 31) * GROUP);
     return QueryHead{src[0], src[1]};
 }
 
@@ -335,11 +376,11 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.p_empty[i], AC_PV_WARPS);
             mbar_init(&sm.q_full[i], 2);
-            mbar_init(&sm.q_empty[i], 5);                   // the row's last MMA and the softmax warps
+            mbar_init(&sm.q_empty[i], 4);                   // the softmax warps: they saw the row's last S
             mbar_init(&sm.r_full[i], 4);
             mbar_init(&sm.r_empty[i], AC_PV_WARPS);
         }
-        mbar_init(&sm.drain, 1);
+        mbar_init(&sm.drain, 2);
         mbar_fence_init();
     }
     if (warp == AC_MMA_WARP) tmem_alloc(&sm.tmem, AT_COLS);
@@ -362,27 +403,45 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
     }
     griddep_launch_dependents();
     griddep_wait();                                         // nothing global is touched before
+    // Every wait is bounded: by `limit` polls, each of which may suspend the thread for about
+    // `nap` ns.  One that runs out flags ERR_TIMEOUT and sets limit to 0: from then on this
+    // thread polls once per wait, issues no copy and no MMA, and takes part in every barrier
+    // and arrival as before, so that all warps reach the end.
     unsigned* err = p.err;
-    const uint32_t limit = wait_limit(err);
+    uint32_t limit = wait_limit(err);
+    const uint32_t nap = limit == SPIN_LIMIT ? 1000u : 0u;
+    auto poll = [&](uint64_t* bar, int phase) {
+        uint32_t ok;
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(ok) : "r"(smem_u32(bar)), "r"(static_cast<uint32_t>(phase & 1)), "r"(nap) : "memory");
+        return ok;
+    };
+    auto wait = [&](uint64_t* bar, int phase) {
+        uint32_t n = 0, ok;
+        do ok = poll(bar, phase);
+        while (!ok && ++n < limit);
+        if (!ok) {
+            limit = 0;
+            atomicOr(err, ERR_TIMEOUT);
+        }
+    };
     const Range range = my_range<AC_THREADS>(p, sm.red);
     if (tid < 2) p.meta[2 * blockIdx.x + tid] = -1;
 
-    bool dead = false;                                      // a wait ran out: no more waiting, no more issuing
-    auto wait = [&](uint64_t* bar, int phase) {
-        if (!dead && !mbar_wait(bar, static_cast<uint32_t>(phase & 1), err, limit)) dead = true;
-    };
     // every role walks the range's rows by itself: it counts tiles, rw rows
     int it = 0, rw = 0;
-    int64_t row = range.row, left = range.count;
-    int tile = range.tile;
+    int row = range.row, left = range.count, tile = range.tile;
     if (left > 0) row = next_row(p, row);
 
     if (warp == AC_TMA_WARP) {
         // ---- producer: runs ahead over the rows, AC_STAGES tiles at most
+        uint64_t policy;
+        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
         auto load_row = [&](bool first) {
             const RowView v = row_view(p, row);
-            const int end = static_cast<int>(min(static_cast<int64_t>(v.tiles), tile + left));
-            const int64_t b = row / p.q_per_seq, off = p.kv_offsets[b];
+            const int end = min(v.tiles, tile + left);
+            const int b = row / p.q_per_seq;
+            const int64_t off = p.kv_offsets[b];
             for (int t0 = tile; t0 < end; t0 += 32) {
                 int y = 0;                                  // each lane looks one tile's row up
                 if (t0 + lane < end) {
@@ -402,12 +461,12 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                     if (lane == 0) {
                         const int st = it % AC_STAGES;
                         if (it >= AC_STAGES) wait(&sm.empty[st], it / AC_STAGES - 1);
-                        if (!dead) {
+                        if (limit) {
                             uint8_t* dst = sm.stage[st];
                             mbar_arrive_expect_tx(&sm.full[st], AC_STAGE_BYTES);
-                            tma_load_2d(dst, &tm_codes, 0, yi, &sm.full[st]);
-                            tma_load_2d(dst + AC_CODE_BYTES / 2, &tm_codes, 128, yi, &sm.full[st]);
-                            tma_load_2d(dst + AC_CODE_BYTES, &tm_scales, 0, yi, &sm.full[st]);
+                            tma_load_stream(dst, &tm_codes, 0, yi, &sm.full[st], policy);
+                            tma_load_stream(dst + AC_CODE_BYTES / 2, &tm_codes, 128, yi, &sm.full[st], policy);
+                            tma_load_stream(dst + AC_CODE_BYTES, &tm_scales, 0, yi, &sm.full[st], policy);
                             sm.issued[st] = it / AC_STAGES + 1;
                         }
                     }
@@ -430,51 +489,39 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                 if (sm.issued[st]) mbar_wait(&sm.full[st], static_cast<uint32_t>((sm.issued[st] - 1) & 1), err);
         }
     } else {
-        // the first row's query: a head per warp; the following rows' by warps 14 and 15
-        if (left > 0) {
-            const int h = warp < AC_TMA_WARP ? warp : warp - 1;
-            put_query(p, sm, 0, h, load_query(p, row, h));
-            if (warp == AC_WARPS - 1) put_query(p, sm, 0, HEADS - 1, load_query(p, row, HEADS - 1));
+        // the first row's query: a head per P V warp; the following rows' by the MMA warps
+        if (left > 0 && warp < AC_PV_WARPS) {
+            put_query(p, sm, 0, warp, load_query(p, row, warp));
             fence_proxy_async_smem();
         }
         __syncthreads();
         tc_fence_after();
-        if (warp >= AC_Q_WARP) {
-            const int h0 = (warp - AC_Q_WARP) * (HEADS / 2);
-            while (left > 0) {
-                if (rw > 0) {
-                    row = next_row(p, row);
-                    const int qb = rw & 1;
-                    if (rw >= 2) wait(&sm.q_empty[qb], (rw >> 1) - 1);
-#pragma unroll 1
-                    for (int h = 0; h < HEADS / 2; h += 4) {
-                        QueryHead v[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = load_query(p, row, h0 + h + i);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) put_query(p, sm, qb, h0 + h + i, v[i]);
-                    }
-                    fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.q_full[rw & 1]);
-                left -= min(static_cast<int64_t>(row_view(p, row).tiles - tile), left);
-                tile = 0;
-                ++row;
-                ++rw;
-            }
-            if (warp == AC_WARPS - 1) empty_rows(p);
-        } else if (warp == AC_MMA_WARP) {
+        if (warp >= AC_MMA_WARP) {
+            const int buf = warp - AC_MMA_WARP;             // tiles of this parity
             const uint64_t dq = umma_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
             const uint64_t dc = umma_desc_sw128(smem_u32(sm.stage[0]), 16, 1024);
             const uint64_t ds = desc_rows16(smem_u32(sm.sf[0][0]));
             while (left > 0) {
-                if (rw > 0) row = next_row(p, row);
-                const int end = static_cast<int>(min(static_cast<int64_t>(row_view(p, row).tiles), tile + left));
-                wait(&sm.q_full[rw & 1], rw >> 1);
-                const uint64_t dqr = dq + (rw & 1) * (2 * AC_QPANEL / 16);
+                const int qb = rw & 1;
+                if (rw > 0) {
+                    row = next_row(p, row);
+                    if (rw >= 2) wait(&sm.q_empty[qb], (rw >> 1) - 1);
+#pragma unroll 1
+                    for (int h = buf * (HEADS / 2); h < (buf + 1) * (HEADS / 2); h += 2) {
+                        const QueryHead a = load_query(p, row, h), b = load_query(p, row, h + 1);
+                        put_query(p, sm, qb, h, a);
+                        put_query(p, sm, qb, h + 1, b);
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.q_full[qb]);
+                const int end = min(row_view(p, row).tiles, tile + left);
+                wait(&sm.q_full[qb], rw >> 1);
+                const uint64_t dqr = dq + qb * (2 * AC_QPANEL / 16);
                 for (int t = tile; t < end; ++t, ++it) {
-                    const int st = it % AC_STAGES, buf = it & 1;
+                    if ((it & 1) != buf) continue;
+                    const int st = it % AC_STAGES;
                     wait(&sm.full[st], it / AC_STAGES);
                     if (it >= 2) wait(&sm.s_empty[buf], (it >> 1) - 1);
                     tc_fence_after();
@@ -493,7 +540,7 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         *reinterpret_cast<uint4*>(sm.sf[buf][s] + 16 * lane) = make_uint4(w[0][s], w[1][s], w[2][s], w[3][s]);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0 && !dead) {
+                    if (lane == 0 && limit) {
                         const uint32_t sfa = tm + AT_SFA + 32 * buf, dst = tm + AT_S + AT_S_STEP * buf;
                         const uint64_t da = dc + st * (AC_STAGE_BYTES / 16), dsb = ds + buf * (8 * 512 / 16);
 #pragma unroll
@@ -504,7 +551,6 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                                      dqr + (s >> 2) * (AC_QPANEL / 16) + (s & 3) * 2, AC_IDESC, sfa + 4 * s,
                                      tm + AT_SFB + 4 * s, s > 0);
                         mma_commit(&sm.s_full[buf]);
-                        if (t + 1 == end) mma_commit(&sm.q_empty[rw & 1]);
                     }
                     __syncwarp();
                 }
@@ -517,78 +563,95 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                 mma_commit(&sm.drain);
                 mbar_wait(&sm.drain, 0, err);
             }
+            if (buf) empty_rows(p);
         } else if (warp >= AC_SM_WARP) {
             // ---- softmax: thread = key
             const int quarter = warp & 3, key = 32 * quarter + lane;
             while (left > 0) {
                 if (rw > 0) row = next_row(p, row);
                 const RowView v = row_view(p, row);
-                const int end = static_cast<int>(min(static_cast<int64_t>(v.tiles), tile + left));
+                const int end = min(v.tiles, tile + left);
                 const int rb = rw & 1;
-                float m[HEADS], l[HEADS];
+                uint64_t l2[HEADS / 2];
 #pragma unroll
-                for (int h = 0; h < HEADS; ++h) {
-                    m[h] = -INFINITY;
-                    l[h] = 0.0f;
-                }
+                for (int i = 0; i < HEADS / 2; ++i) l2[i] = 0;
                 wait(&sm.q_full[rb], rw >> 1);               // f
+                if (rw >= 2) wait(&sm.r_empty[rb], (rw >> 1) - 1);
+                if (warp == AC_SM_WARP && lane < HEADS) sm.minus_m[rb][lane] = 0.0f;     // the first tile sets it
+                named_barrier(BAR_MAX, 128);
                 for (int t = tile; t < end; ++t, ++it) {
-                    const int st = it % AC_STAGES, buf = it & 1;
-                    const bool vis = visible(p, v, v.pos(t) + key);
+                    const int st = it % AC_STAGES, buf = it & 1, base = v.pos(t);
+                    const bool vis = visible(p, v, base + key);
+                    const bool all = base + CACHE_TILE <= v.n_vis && (base >= v.w_beg || base + CACHE_TILE <= p.sinks);
                     wait(&sm.s_full[buf], it >> 1);
                     tc_fence_after();
-                    float s[HEADS];
+                    uint64_t s[HEADS / 2];                  // the digits' columns summed, two heads a pair
                     const uint32_t src = tm + (static_cast<uint32_t>(32 * quarter) << 16) + AT_S + AT_S_STEP * buf;
 #pragma unroll
-                    for (int i = 0; i < AC_N / 32; ++i) {
-                        uint32_t r[32];
-                        tmem_ld32(src + 32 * i, r);
+                    for (int i = 0; i < AC_DIGITS; ++i) {
+                        uint32_t r[HEADS];
+                        tmem_ld16(src + HEADS * i, r);
 #pragma unroll
-                        for (int h = 0; h < HEADS; ++h) {
-                            const float two = __uint_as_float(r[h]) + __uint_as_float(r[16 + h]);
-                            s[h] = i ? s[h] + two : two;
+                        for (int h = 0; h < HEADS / 2; ++h) {
+                            const uint64_t one = pack2(__uint_as_float(r[2 * h]), __uint_as_float(r[2 * h + 1]));
+                            s[h] = i ? add2(s[h], one) : one;
                         }
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.s_empty[buf]);
-                    float d = -INFINITY;
+                    float x[HEADS];                         // logits less the reference, in powers of two
+                    scale_heads(s, sm.f[rb], sm.minus_m[rb], x);
+                    if (!all) {
 #pragma unroll
-                    for (int h = 0; h < HEADS; ++h) {
-                        s[h] = vis ? s[h] * sm.f[rb][h] : -INFINITY;
-                        d = fmaxf(d, s[h] - m[h]);           // (-inf) - (-inf): NaN, which fmaxf drops
+                        for (int h = 0; h < HEADS; ++h) x[h] = vis ? x[h] : -INFINITY;
                     }
+                    float d = x[0];
+#pragma unroll
+                    for (int h = 1; h < HEADS; ++h) d = fmaxf(d, x[h]);
                     if (it >= 2) wait(&sm.p_empty[buf], (it >> 1) - 1);
-                    const bool moved = vote_barrier(BAR_VOTE, 128, d > AC_GAP);
-                    if (moved) {
-                        const float top = reduce_heads<true>(s);
+                    const bool first = t == tile;
+                    if (vote_barrier(BAR_VOTE, 128, d > AC_GAP + AC_SHIFT || first)) {
+                        // back to plain logits, their maximum over the tile's keys, and a new reference
+#pragma unroll
+                        for (int h = 0; h < HEADS; ++h) x[h] = vis ? x[h] - sm.minus_m[rb][h] : -INFINITY;
+                        const float top = reduce_heads<true>(x);
                         if (!(lane & 1)) sm.part_m[quarter][head_of(lane)] = top;
                         named_barrier(BAR_MAX, 128);
+                        float mine = 0.0f;
 #pragma unroll
-                        for (int h = 0; h < HEADS; ++h) {
-                            const float mn = fmaxf(fmaxf(fmaxf(sm.part_m[0][h], sm.part_m[1][h]),
-                                                         fmaxf(sm.part_m[2][h], sm.part_m[3][h])), m[h]);
-                            const float a = mn == -INFINITY ? 1.0f : fast_exp2(m[h] - mn);
-                            m[h] = mn;
-                            l[h] *= a;
-                            if (tid == 32 * AC_SM_WARP) sm.alpha[buf][h] = a;
+                        for (int h = 0; h < HEADS; h += 2) {
+                            float2 l = unpack2(l2[h / 2]);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float old = first ? -INFINITY : -sm.minus_m[rb][h + e];
+                                const float mn = fmaxf(fmaxf(fmaxf(sm.part_m[0][h + e], sm.part_m[1][h + e]),
+                                                             fmaxf(sm.part_m[2][h + e], sm.part_m[3][h + e])) - AC_SHIFT, old);
+                                const float a = first ? 0.0f : fast_exp2(old - mn);
+                                if (e) l.y *= a;
+                                else l.x *= a;
+                                if (lane == h + e) mine = mn;
+                                x[h + e] -= mn;
+                            }
+                            l2[h / 2] = pack2(l.x, l.y);
                         }
+                        named_barrier(BAR_MAX, 128);          // everyone has read the old ones
+                        if (warp == AC_SM_WARP && lane < HEADS) sm.minus_m[rb][lane] = -mine;
+                        named_barrier(BAR_MAX, 128);
                     }
-                    if (tid == 32 * AC_SM_WARP) sm.moved[buf] = moved;
+                    if (warp == AC_SM_WARP && lane < HEADS) sm.ref[buf][lane] = -sm.minus_m[rb][lane];
                     uint32_t pk[HEADS / 2];
 #pragma unroll
                     for (int h = 0; h < HEADS; h += 2) {
-                        const float a = vis ? fast_exp2(s[h] - m[h] + AC_SHIFT) : 0.0f;
-                        const float b = vis ? fast_exp2(s[h + 1] - m[h + 1] + AC_SHIFT) : 0.0f;
-                        l[h] += a;
-                        l[h + 1] += b;
+                        const float a = fast_exp2(x[h]), b = fast_exp2(x[h + 1]);
+                        l2[h / 2] = add2(l2[h / 2], pack2(a, b));
                         const __half2 two = __floats2half2_rn(a, b);
                         pk[h / 2] = *reinterpret_cast<const uint32_t*>(&two);
                     }
                     uint8_t* dst = sm.p[buf] + key * 32;
-                    const int x = ((key >> 2) & 1) << 4;
-                    *reinterpret_cast<uint4*>(dst + x) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                    *reinterpret_cast<uint4*>(dst + (x ^ 16)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                    const int swap = ((key >> 2) & 1) << 4;
+                    *reinterpret_cast<uint4*>(dst + swap) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    *reinterpret_cast<uint4*>(dst + (swap ^ 16)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
                     if (!vis) {
                         // rows behind the sequence or its mask may hold any bytes, NaN scales among
                         // them: 0 x NaN must not reach O
@@ -596,16 +659,18 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         z[0] = z[1] = make_uint4(0u, 0u, 0u, 0u);
                         fence_proxy_async_smem();            // before the next copy into this stage
                     }
+                    wait(&sm.full[st], it / AC_STAGES);      // P V reads the tile on this word
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.p_full[buf]);
                 }
-                if (rw >= 2) wait(&sm.r_empty[rb], (rw >> 1) - 1);
+                float l[HEADS];
+#pragma unroll
+                for (int h = 0; h < HEADS; h += 2) {
+                    const float2 u = unpack2(l2[h / 2]);
+                    l[h] = u.x, l[h + 1] = u.y;
+                }
                 const float sum = reduce_heads<false>(l);
                 if (!(lane & 1)) sm.l[rb][quarter][head_of(lane)] = sum;
-                if (tid == 32 * AC_SM_WARP) {
-#pragma unroll
-                    for (int h = 0; h < HEADS; ++h) sm.m[rb][h] = m[h];
-                }
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&sm.r_full[rb]);
@@ -617,67 +682,69 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                 ++rw;
             }
         } else {
-            // ---- P V: warp owns channels 128 (w % 4) .. + 127 of keys 64 (w / 4) .. + 63; lane
-            // (g, t) converts channels 16 g .. + 15 of those (one scale group) of the keys of its
-            // B fragments, n-tile i being channel i of every group
-            const int wq = warp & 3, kh = warp >> 2, g = lane >> 2, t4 = lane & 3;
-            const uint32_t code_off = (wq >> 1) * (AC_CODE_BYTES / 2) + (g & 1) * 8;
-            const uint32_t chunk = (wq & 1) * 4 + (g >> 1);
+            // ---- P V: warp owns channels 64 (w % 8) .. + 63 of keys 64 (w / 8) .. + 63; lane (g, t)
+            // converts channels 8 g .. + 7 of those (half a scale group) of the keys of its B
+            // fragments, n-tile i being channel i of every such half group
+            const int wd = warp & 7, kh = warp >> 3, g = lane >> 2, t4 = lane & 3;
+            const uint32_t code_off = (wd >> 2) * (AC_CODE_BYTES / 2) + (g & 3) * 4;
+            const uint32_t chunk = (wd & 3) * 2 + (g >> 2);
             while (left > 0) {
                 if (rw > 0) row = next_row(p, row);
                 const int tiles = row_view(p, row).tiles;
-                const int end = static_cast<int>(min(static_cast<int64_t>(tiles), tile + left));
-                float o[16][4] = {};
+                const int end = min(tiles, tile + left);
+                float o[8][4] = {};
+                float m0 = -INFINITY, m1 = -INFINITY;        // references of heads g, g + 8 that o stands at
+                uint32_t ready = 0;                          // P of the next tile seen already
                 for (int t = tile; t < end; ++t, ++it) {
                     const int st = it % AC_STAGES, buf = it & 1;
-                    wait(&sm.full[st], it / AC_STAGES);
-                    wait(&sm.p_full[buf], it >> 1);
-                    if (sm.moved[buf]) {
-                        const float a0 = sm.alpha[buf][g], a1 = sm.alpha[buf][g + 8];
+                    if (!ready) wait(&sm.p_full[buf], it >> 1);
+                    const uint8_t* codes = sm.stage[st] + code_off;
+                    const uint8_t* scales = sm.stage[st] + AC_CODE_BYTES + wd * 4 + (g >> 1);
+                    const uint32_t pa = smem_u32(sm.p[buf]);
+                    // step ks + 1's operands are loaded while step ks is multiplied
+                    uint32_t a[2][4], c[2][4], sc[2][4];
+                    auto load_step = [&](int ks) {
+                        const int kb = 64 * kh + 16 * ks, n = ks & 1;
+                        const int ak = kb + ((lane >> 4) << 3) + (lane & 7);
+                        ldmatrix_x4_trans(a[n], pa + ak * 32 + ((((lane >> 3) ^ (ak >> 2)) & 1) << 4));
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int j = 0; j < 4; ++j) {
+                            const int key = kb + 2 * t4 + (j & 1) + 8 * (j >> 1);
+                            c[n][j] = *reinterpret_cast<const uint32_t*>(codes + key * 128 + ((chunk ^ (key & 7)) << 4));
+                            sc[n][j] = scales[key * ROW_SCALES];
+                        }
+                    };
+                    load_step(0);
+                    const float n0 = sm.ref[buf][g], n1 = sm.ref[buf][g + 8];
+                    if (__any_sync(0xFFFFFFFFu, n0 != m0 || n1 != m1)) {
+                        const float a0 = n0 == m0 ? 1.0f : fast_exp2(m0 - n0), a1 = n1 == m1 ? 1.0f : fast_exp2(m1 - n1);
+                        m0 = n0;
+                        m1 = n1;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
                             o[i][0] *= a0;
                             o[i][1] *= a0;
                             o[i][2] *= a1;
                             o[i][3] *= a1;
                         }
                     }
-                    const uint8_t* codes = sm.stage[st] + code_off;
-                    const uint8_t* scales = sm.stage[st] + AC_CODE_BYTES + wq * 8 + g;
-                    const uint32_t pa = smem_u32(sm.p[buf]);
-#pragma unroll 2
+#pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
-                        const int kb = 64 * kh + 16 * ks;
-                        uint32_t a[4];
-                        {
-                            const int key = kb + ((lane >> 4) << 3) + (lane & 7);
-                            ldmatrix_x4_trans(a, pa + key * 32 + ((((lane >> 3) ^ (key >> 2)) & 1) << 4));
-                        }
-                        uint2 c[4];
-                        uint32_t sc[4];
+                        const int n = ks & 1;
+                        if (ks < 3) load_step(ks + 1);
+                        else ready = t + 1 < end ? poll(&sm.p_full[buf ^ 1], (it + 1) >> 1) : 0u;
+                        const uint32_t s0 = e4m3x2_to_f16x2(static_cast<uint16_t>(sc[n][0] | (sc[n][1] << 8)));
+                        const uint32_t s1 = e4m3x2_to_f16x2(static_cast<uint16_t>(sc[n][2] | (sc[n][3] << 8)));
+                        // two keys' codes interleaved: byte i of ev / od = channel 2 i / 2 i + 1 of both
+                        uint32_t e0[4], e1[4], d0[4], d1[4];
+                        e2m1x8_to_f16((c[n][0] & 0x0F0F0F0Fu) | ((c[n][1] << 4) & 0xF0F0F0F0u), e0);
+                        e2m1x8_to_f16((c[n][2] & 0x0F0F0F0Fu) | ((c[n][3] << 4) & 0xF0F0F0F0u), e1);
+                        e2m1x8_to_f16(((c[n][0] >> 4) & 0x0F0F0F0Fu) | (c[n][1] & 0xF0F0F0F0u), d0);
+                        e2m1x8_to_f16(((c[n][2] >> 4) & 0x0F0F0F0Fu) | (c[n][3] & 0xF0F0F0F0u), d1);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int key = kb + 2 * t4 + (j & 1) + 8 * (j >> 1);
-                            c[j] = *reinterpret_cast<const uint2*>(codes + key * 128 + ((chunk ^ (key & 7)) << 4));
-                            sc[j] = scales[key * ROW_SCALES];
-                        }
-                        const uint32_t s0 = e4m3x2_to_f16x2(static_cast<uint16_t>(sc[0] | (sc[1] << 8)));
-                        const uint32_t s1 = e4m3x2_to_f16x2(static_cast<uint16_t>(sc[2] | (sc[3] << 8)));
-#pragma unroll
-                        for (int hw = 0; hw < 2; ++hw) {     // channels 8 hw .. + 7
-                            const uint32_t a0 = hw ? c[0].y : c[0].x, a1 = hw ? c[1].y : c[1].x;
-                            const uint32_t b0 = hw ? c[2].y : c[2].x, b1 = hw ? c[3].y : c[3].x;
-                            // two keys' codes interleaved: byte i of ev / od = channel 2 i / 2 i + 1 of both
-                            uint32_t e0[4], e1[4], d0[4], d1[4];
-                            e2m1x8_to_f16((a0 & 0x0F0F0F0Fu) | ((a1 << 4) & 0xF0F0F0F0u), e0);
-                            e2m1x8_to_f16(((a0 >> 4) & 0x0F0F0F0Fu) | (a1 & 0xF0F0F0F0u), d0);
-                            e2m1x8_to_f16((b0 & 0x0F0F0F0Fu) | ((b1 << 4) & 0xF0F0F0F0u), e1);
-                            e2m1x8_to_f16(((b0 >> 4) & 0x0F0F0F0Fu) | (b1 & 0xF0F0F0F0u), d1);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                mma_16816(o[8 * hw + 2 * i], a, mul_f16x2(e0[i], s0), mul_f16x2(e1[i], s1));
-                                mma_16816(o[8 * hw + 2 * i + 1], a, mul_f16x2(d0[i], s0), mul_f16x2(d1[i], s1));
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            mma_16816(o[2 * i], a[n], mul_f16x2(e0[i], s0), mul_f16x2(e1[i], s1));
+                            mma_16816(o[2 * i + 1], a[n], mul_f16x2(d0[i], s0), mul_f16x2(d1[i], s1));
                         }
                     }
                     __syncwarp();
@@ -686,73 +753,65 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         mbar_arrive(&sm.empty[st]);
                     }
                 }
-                // ---- the key halves: warps 4-7 hand n-tiles 0 .. 7 over and take 8 .. 15
+                // ---- the key halves: warps 8-15 hand n-tiles 0 .. 3 over and take 4 .. 7
                 const bool whole = tile == 0 && end == tiles;
                 const int slot = 2 * blockIdx.x + (tile == 0 ? 1 : 0);     // 0: the row this range starts in
                 float* part = p.part + static_cast<int64_t>(slot) * CACHE_PART_FLOATS;
                 const int rb = rw & 1;
+                wait(&sm.r_full[rb], rw >> 1);
                 if (kh) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) sm.x[wq][i][lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                    for (int i = 0; i < 4; ++i) sm.x[wd][i][lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
                 }
-                named_barrier(BAR_PV + wq, 64);
+                named_barrier(BAR_PV + wd, 64);
                 if (!kh) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 u = sm.x[wq][i][lane];
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 u = sm.x[wd][i][lane];
                         o[i][0] += u.x, o[i][1] += u.y, o[i][2] += u.z, o[i][3] += u.w;
-                        sm.x[wq][i][lane] = make_float4(o[8 + i][0], o[8 + i][1], o[8 + i][2], o[8 + i][3]);
+                        sm.x[wd][i][lane] = make_float4(o[4 + i][0], o[4 + i][1], o[4 + i][2], o[4 + i][3]);
                     }
                 }
-                named_barrier(BAR_PV + wq, 64);
+                named_barrier(BAR_PV + wd, 64);
                 if (kh) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 u = sm.x[wq][i][lane];
-                        o[i][0] = o[8 + i][0] + u.x, o[i][1] = o[8 + i][1] + u.y;
-                        o[i][2] = o[8 + i][2] + u.z, o[i][3] = o[8 + i][3] + u.w;
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 u = sm.x[wd][i][lane];
+                        o[i][0] = o[4 + i][0] + u.x, o[i][1] = o[4 + i][1] + u.y;
+                        o[i][2] = o[4 + i][2] + u.z, o[i][3] = o[4 + i][3] + u.w;
                     }
                 }
-                wait(&sm.r_full[rb], rw >> 1);
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     const int h = g + 8 * hh;
                     const float ls = sm.l[rb][0][h] + sm.l[rb][1][h] + sm.l[rb][2][h] + sm.l[rb][3][h];
                     const float inv = whole ? 1.0f / ls : 1.0f;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int ch = 128 * wq + 16 * (2 * t4 + e) + 8 * kh;
-                        float val[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) val[i] = o[i][2 * hh + e] * inv;
-                        const int64_t at = (row * HEADS + h) * D + ch;
+                    for (int e = 0; e < 2; ++e) {            // channels 8 (2 t + e) + 4 kh .. + 3 of the warp's
+                        const int ch = 64 * wd + 8 * (2 * t4 + e) + 4 * kh;
+                        const float4 val = make_float4(o[0][2 * hh + e] * inv, o[1][2 * hh + e] * inv, o[2][2 * hh + e] * inv,
+                                                       o[3][2 * hh + e] * inv);
+                        const int64_t at = (static_cast<int64_t>(row) * HEADS + h) * D + ch;
                         if (whole && !p.out_f32) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const __nv_bfloat162 two = __floats2bfloat162_rn(val[2 * i], val[2 * i + 1]);
-                                w[i] = *reinterpret_cast<const uint32_t*>(&two);
-                            }
-                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                            const __nv_bfloat162 a = __floats2bfloat162_rn(val.x, val.y), b = __floats2bfloat162_rn(val.z, val.w);
+                            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+                                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
                         } else {
-                            float4* dst = reinterpret_cast<float4*>(whole ? static_cast<float*>(p.out) + at
-                                                                          : part + 2 * HEADS + h * D + ch);
-                            dst[0] = make_float4(val[0], val[1], val[2], val[3]);
-                            dst[1] = make_float4(val[4], val[5], val[6], val[7]);
+                            *reinterpret_cast<float4*>(whole ? static_cast<float*>(p.out) + at : part + 2 * HEADS + h * D + ch) = val;
                         }
                     }
                     if (warp == 0 && t4 == 0) {
                         if (!whole) {
-                            part[h] = sm.m[rb][h] - AC_SHIFT;
+                            part[h] = -sm.minus_m[rb][h];
                             part[HEADS + h] = ls;
                         } else if (p.lse) {
-                            p.lse[row * HEADS + h] = (sm.m[rb][h] - AC_SHIFT + log2f(ls)) * LN2;
+                            p.lse[static_cast<int64_t>(row) * HEADS + h] = (log2f(ls) - sm.minus_m[rb][h]) * LN2;
                         }
                     }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.r_empty[rb]);
-                if (!whole && tid == 0) p.meta[slot] = static_cast<int32_t>(row);
+                if (!whole && tid == 0) p.meta[slot] = row;
                 left -= end - tile;
                 tile = 0;
                 ++row;
