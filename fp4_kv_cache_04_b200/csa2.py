@@ -348,12 +348,18 @@ def _same_device(args, *tensors) -> None:
     devs = {t.device for t in tensors if t is not None}
     _need(len(devs) == 1, f"tensors on different devices: {sorted(map(str, devs))}")
     args.device = devs.pop().index
+    args.ref = ctypes.byref(args)
     args.tensors = tensors                     # alive as long as the block that points at them
 
 
-def _on_device(args, where: str) -> None:
-    _need(torch.cuda.current_device() == args.device,
-          f"{where}: the tensors are on cuda:{args.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _launch(fn, args, stream, where: str) -> None:
+    """Calls fn(args, stream); the current device must be the one the block's tensors are on."""
+    dev = torch.cuda.current_device()
+    if dev != args.device:
+        raise ValueError(f"libcsa2: {where}: the tensors are on cuda:{args.device}, the current device is cuda:{dev}")
+    status = fn(args.ref, _stream(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        raise Csa2Error(status, where)
 
 
 def _vec(t: torch.Tensor | None, dtype, n: int, what: str) -> int | None:
@@ -399,8 +405,7 @@ def rope_args(*, x: torch.Tensor, out: torch.Tensor, pos: torch.Tensor | None = 
 
 def norm_rope(args: RopeArgs, stream=None) -> None:
     """Head norm and rotary positions in one pass (csa2_norm_rope)."""
-    _on_device(args, "norm_rope")
-    _check(_lib.csa2_norm_rope(ctypes.byref(args), _stream(stream)), "csa2_norm_rope")
+    _launch(_lib.csa2_norm_rope, args, stream, "csa2_norm_rope")
 
 
 def append_args(*, latent: torch.Tensor, pos: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
@@ -449,21 +454,29 @@ def append_args(*, latent: torch.Tensor, pos: torch.Tensor, codes: torch.Tensor,
 
 def append_rope(args: AppendArgs, stream=None) -> None:
     """Cache append with norm and rotation on the way (csa2_append_rope)."""
-    _on_device(args, "append_rope")
-    _check(_lib.csa2_append_rope(ctypes.byref(args), _stream(stream)), "csa2_append_rope")
+    _launch(_lib.csa2_append_rope, args, stream, "csa2_append_rope")
 
 
 def dequantize_kv(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, src_row: torch.Tensor | None = None,
                   stream=None) -> None:
     """Cache rows (src_row int64 [n], or rows 0 .. n-1) -> bf16 out [n][512]."""
-    _need(codes.dtype == torch.uint8 and scales.dtype == torch.uint8 and codes.shape[0] == scales.shape[0] and
-          codes.shape[1] == ROW_CODES and scales.shape[1] == ROW_SCALES, "codes uint8 [rows][256], scales uint8 [rows][32]")
-    _need(out.dtype == torch.bfloat16 and out.dim() == 2 and out.shape[1] == D, "out is bf16 [n][512]")
-    _need(out.device == codes.device == scales.device and out.device.index == torch.cuda.current_device(),
-          "dequantize_kv: the tensors are not on the current device")
-    _check(_lib.csa2_dequantize_kv(_ptr(codes), _ptr(scales), codes.shape[0],
-                                   _vec(src_row, torch.int64, out.shape[0], "src_row"), out.shape[0], _ptr(out),
-                                   _stream(stream)), "csa2_dequantize_kv")
+    n, d = out.shape
+    rows, wide = codes.shape
+    if not (codes.dtype is scales.dtype is torch.uint8 and out.dtype is torch.bfloat16 and d == D and wide == ROW_CODES and
+            scales.shape == (rows, ROW_SCALES) and (src_row is None or src_row.dtype is torch.int64 and src_row.numel() == n)):
+        raise ValueError("libcsa2: codes uint8 [rows][256], scales uint8 [rows][32], out bf16 [n][512], src_row int64 [n]")
+    dev = torch.cuda.current_device()
+    if not codes.get_device() == scales.get_device() == out.get_device() == dev or (
+            src_row is not None and src_row.get_device() != dev):
+        raise ValueError("libcsa2: dequantize_kv: the tensors are not on the current device")
+    if not (codes.is_contiguous() and scales.is_contiguous() and out.is_contiguous() and
+            (src_row is None or src_row.is_contiguous())):
+        raise ValueError("libcsa2 takes contiguous tensors")
+    status = _lib.csa2_dequantize_kv(codes.data_ptr(), scales.data_ptr(), rows, None if src_row is None else src_row.data_ptr(),
+                                     n, out.data_ptr(),
+                                     _stream(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        raise Csa2Error(status, "csa2_dequantize_kv")
 
 
 def cache_args(*, batch: int, max_n: int, kv_offsets: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
@@ -497,5 +510,4 @@ def cache_workspace_size(args: CacheArgs) -> int:
 
 def attend_cache(args: CacheArgs, stream=None) -> None:
     """Attention over the whole cache or a window of it (csa2_attend_cache)."""
-    _on_device(args, "attend_cache")
-    _check(_lib.csa2_attend_cache(ctypes.byref(args), _stream(stream)), "csa2_attend_cache")
+    _launch(_lib.csa2_attend_cache, args, stream, "csa2_attend_cache")

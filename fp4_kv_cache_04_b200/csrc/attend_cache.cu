@@ -931,24 +931,12 @@ csa2_status launch_attend_cache(const CacheParams& p, const CUtensorMap& codes, 
     const int smem = static_cast<int>(sizeof(CacheSmem) + 1024);
     if (!opt_in_smem(reinterpret_cast<const void*>(attend_cache_kernel), smem))
         return check_launch("attend_cache_kernel smem attribute");
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.ranges));
-    cfg.blockDim = dim3(AC_THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, attend_cache_kernel, p, codes, scales);
+    launch_dependent(attend_cache_kernel, dim3(static_cast<unsigned>(p.ranges)), AC_THREADS, smem, stream, p, codes, scales);
     csa2_status st = check_launch("attend_cache_kernel");
     if (st != CSA2_OK || p.ranges == 1 || p.whole_rows) return st;
     const int64_t rows = static_cast<int64_t>(p.batch) * p.q_per_seq;
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(rows, p.ranges - 1)), AJ_SLICES);
-    cfg.blockDim = dim3(AJ_THREADS);
-    cfg.dynamicSmemBytes = 0;
-    cudaLaunchKernelEx(&cfg, join_cache_kernel, p);
+    launch_dependent(join_cache_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(rows, p.ranges - 1)), AJ_SLICES), AJ_THREADS, 0,
+                     stream, p);
     return check_launch("join_cache_kernel");
 }
 

@@ -8,6 +8,24 @@
 
 namespace csa2 {
 
+// Launch as a programmatic dependent of the kernel before it on the stream: the kernel must
+// call griddep_wait() before it touches global memory.
+template <typename... Params, typename... Args>
+inline void launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                             const Args&... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // FP4 rows back to bf16 (rows outside [0, total_rows) give zeros).
 csa2_status launch_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t total_rows, const int64_t* src_row,
                               int64_t n, uint16_t* out, cudaStream_t stream);

@@ -14,6 +14,7 @@
 
 #include "dense.cuh"
 #include "row_formats.cuh"
+#include "tc.cuh"
 
 namespace csa2 {
 
@@ -91,46 +92,47 @@ append_kernel(const uint16_t* __restrict__ latent, const float* __restrict__ pro
     store_idx_row(k, lane, idx_k + out_row * IDX_DIM, idx_kscale + out_row);
 }
 
-// FP4 rows back to bf16: one lane per 16-channel group, 8 code bytes and a scale in, 32
-// bytes out; four rows per warp in flight.  e2m1 x e4m3 has at most 6 significant bits, so
-// the fp32 product and its bf16 rounding are both exact.
+// FP4 rows back to bf16: a row is 64 pieces of 8 channels; lane l takes pieces l and l + 32,
+// so that a warp's loads (4 B) and stores (16 B) are contiguous, four rows in flight.  e2m1 x
+// e4m3 has at most 6 significant bits, so the fp32 product and its bf16 rounding are exact.
 constexpr int DQ_ROWS = 4;
 
 __global__ void __launch_bounds__(256)
-dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t total_rows,
-                  const int64_t* __restrict__ src_row, int64_t n, uint16_t* __restrict__ out) {
+dequantize_kernel(const uint8_t* codes, const uint8_t* scales, int64_t total_rows, const int64_t* src_row, int64_t n,
+                  uint16_t* out) {
+    griddep_launch_dependents();
+    griddep_wait();
     const int lane = threadIdx.x & 31;
     const int64_t first = (static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32) * DQ_ROWS;
-    uint2 c[DQ_ROWS];
-    uint32_t sc[DQ_ROWS];
+    uint32_t c[DQ_ROWS][2], sc[DQ_ROWS][2];
 #pragma unroll
     for (int r = 0; r < DQ_ROWS; ++r) {
-        c[r] = make_uint2(0u, 0u);
-        sc[r] = 0u;
-        if (first + r < n) {
-            const int64_t row = src_row ? __ldg(src_row + first + r) : first + r;
-            if (row >= 0 && row < total_rows) {
-                c[r] = __ldg(reinterpret_cast<const uint2*>(codes + row * ROW_CODES) + lane);
-                sc[r] = __ldg(scales + row * ROW_SCALES + lane);
-            }
+        int64_t row = -1;
+        if (first + r < n) row = src_row ? src_row[first + r] : first + r;
+        const bool ok = row >= 0 && row < total_rows;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            c[r][k] = ok ? reinterpret_cast<const uint32_t*>(codes + row * ROW_CODES)[lane + 32 * k] : 0u;
+            sc[r][k] = ok ? scales[row * ROW_SCALES + lane / 2 + 16 * k] : 0u;
         }
     }
 #pragma unroll
     for (int r = 0; r < DQ_ROWS; ++r) {
         if (first + r >= n) return;
-        const float s = e4m3_to_float(static_cast<uint8_t>(sc[r]));
-        uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t byte = ((i < 4 ? c[r].x : c[r].y) >> (8 * (i & 3))) & 0xFFu;
-            const __half2_raw hr = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
-            const float2 f = __half22float2(__half2(hr));
-            const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * s, f.y * s);
-            w[i] = *reinterpret_cast<const uint32_t*>(&v);
+        for (int k = 0; k < 2; ++k) {
+            const float s = e4m3_to_float(static_cast<uint8_t>(sc[r][k]));
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __half2_raw hr =
+                    __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>((c[r][k] >> (8 * i)) & 0xFFu), __NV_E2M1);
+                const float2 f = __half22float2(__half2(hr));
+                const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * s, f.y * s);
+                w[i] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            __stcs(reinterpret_cast<uint4*>(out + (first + r) * D) + lane + 32 * k, make_uint4(w[0], w[1], w[2], w[3]));
         }
-        uint4* dst = reinterpret_cast<uint4*>(out + (first + r) * D + lane * GROUP);
-        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
 }
 
@@ -140,8 +142,8 @@ csa2_status launch_dequantize(const uint8_t* codes, const uint8_t* scales, int64
                               int64_t n, uint16_t* out, cudaStream_t stream) {
     if (n == 0) return CSA2_OK;
     const int rows_per_block = 8 * DQ_ROWS;
-    dequantize_kernel<<<static_cast<unsigned>(ceil_div(n, rows_per_block)), 256, 0, stream>>>(codes, scales, total_rows,
-                                                                                           src_row, n, out);
+    launch_dependent(dequantize_kernel, dim3(static_cast<unsigned>(ceil_div(n, rows_per_block))), 256, 0, stream, codes, scales,
+                     total_rows, src_row, n, out);
     return check_launch("dequantize_kernel");
 }
 

@@ -8,6 +8,7 @@
 // The angle is formed in 64 bits and reduced there to a fraction of a turn, so a position
 // of 2^30 still has its angle to 2^-22 of a turn; only then does sincospi see it.
 #include "dense.cuh"
+#include "tc.cuh"
 #include "row_formats.cuh"
 
 namespace csa2 {
@@ -87,6 +88,8 @@ template <int TI, int TO, int ITEMS, bool HALF>
 __global__ void __launch_bounds__(NR_THREADS)
 norm_rope_kernel(RopeParams p, int rows_per_block, int lanes) {
     extern __shared__ float2 nr_smem[];        // [rows_per_block][rope_dim / 2], then vectors
+    griddep_launch_dependents();
+    griddep_wait();
     const int pairs = p.rope_dim / 2;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows_per_block;
     const int n_rows = static_cast<int>(min(static_cast<int64_t>(rows_per_block), p.rows - row0));
@@ -202,20 +205,73 @@ __device__ __forceinline__ uint16_t round_bf16(float hi, float lo) {
     return *reinterpret_cast<const uint16_t*>(&h);
 }
 
+// sin and cos of 2 pi t, |t| <= 1/2, in 64 bits: the nearest quarter turn taken off leaves
+// |x| <= pi/4, where the Taylor series to x^13 and x^14 are off by less than 2^-45.
+__device__ __forceinline__ double2 turn_cos_sin(double t) {
+    const double q = rint(4.0 * t);
+    const double x = (t - 0.25 * q) * 6.283185307179586477, z = x * x;
+    double s = 1.0 / 6227020800.0, c = -1.0 / 87178291200.0;
+    s = fma(s, z, -1.0 / 39916800.0);
+    c = fma(c, z, 1.0 / 479001600.0);
+    s = fma(s, z, 1.0 / 362880.0);
+    c = fma(c, z, -1.0 / 3628800.0);
+    s = fma(s, z, -1.0 / 5040.0);
+    c = fma(c, z, 1.0 / 40320.0);
+    s = fma(s, z, 1.0 / 120.0);
+    c = fma(c, z, -1.0 / 720.0);
+    s = fma(s, z, -1.0 / 6.0);
+    c = fma(c, z, 1.0 / 24.0);
+    s = fma(s * z, x, x);
+    c = fma(c, z, -0.5);
+    c = fma(c, z, 1.0);
+    const int n = static_cast<int>(q) & 3;                  // quarter turns
+    const double cc = (n & 1) ? s : c, ss = (n & 1) ? c : s;
+    return make_double2(n == 1 || n == 2 ? -cc : cc, n >= 2 ? -ss : ss);
+}
+
 constexpr int AR_WARPS = 8;
+
+struct AppendSmem {
+    float2 y[D];                               // normed channels as hi + lo, the rotated ones only
+    uint16_t h[D];                             // those turned and rounded to bf16
+};
 
 // One warp per token, one lane per 16-channel group (as in quantize.cu).  The FP4 codes
 // change by a whole step at a border, so the bf16 value they are made of is the real
-// number's rounding: the sum of squares and 1/sqrt in 64 bits, x * (w * r) as an fp32 pair
-// hi + lo (its error ~2^-45), the rotated channels in 64 bits.  Shared memory per warp:
-// 256 (cos, sin) double pairs and, for the half-split pairing, the 512 normed channels.
+// number's rounding: the sum of squares in 64 bits, 1/sqrt by one 64-bit Newton step from
+// the fp32 one (2^-43), x * (w * r) as an fp32 pair hi + lo (its error ~2^-45), the rotated
+// channels in 64 bits, a pair per lane and turn, exchanged through shared memory.
 template <int TI>
 __global__ void __launch_bounds__(32 * AR_WARPS)
 append_rope_kernel(AppendParams p) {
-    extern __shared__ double2 ar_smem[];
+    extern __shared__ AppendSmem ar_smem[];
+    griddep_launch_dependents();
+    griddep_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int64_t i = static_cast<int64_t>(blockIdx.x) * AR_WARPS + warp;
     if (i >= p.n) return;
+    const auto* src = static_cast<const typename Elem<TI>::type*>(p.latent) + i * p.latent_stride + lane * GROUP;
+    float x[16];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        float a[8];
+        load8<TI>(src + 8 * q, a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[8 * q + j] = a[j];
+    }
+    float w[16];
+    if (p.norm && p.weight) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float a[8];
+            load8<CSA2_T_F32>(p.weight + lane * GROUP + 8 * q, a);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[8 * q + j] = a[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[j] = 1.0f;
+    }
     const int64_t pos = p.pos[i];
     if (pos < 0) return;
     const int64_t b = p.seq ? p.seq[i] : i;
@@ -223,7 +279,7 @@ append_rope_kernel(AppendParams p) {
     if (b >= 0 && b < p.batch) {
         if (p.rows.page_table) {
             if (pos < static_cast<int64_t>(p.rows.pages_per_seq) * p.rows.page_rows) {
-                const int64_t pg = __ldg(p.rows.page_table + b * p.rows.pages_per_seq + pos / p.rows.page_rows);
+                const int64_t pg = p.rows.page_table[b * p.rows.pages_per_seq + pos / p.rows.page_rows];
                 if (pg >= 0) row = pg * p.rows.page_rows + pos % p.rows.page_rows;
             }
         } else {
@@ -236,25 +292,6 @@ append_rope_kernel(AppendParams p) {
         return;
     }
 
-    const int pairs = p.rope_dim / 2;
-    double2* cs = ar_smem + warp * (pairs + (p.half && pairs ? D / 2 : 0));
-    for (int k = lane; k < pairs; k += 32) {
-        double s, c;
-        sincospi(2.0 * turn_fraction(pos, p.inv_freq[k]), &s, &c);
-        cs[k] = make_double2(c, s);
-    }
-
-    const auto* src = static_cast<const typename Elem<TI>::type*>(p.latent) + i * p.latent_stride + lane * GROUP;
-    float x[16];
-    {
-        float a[8];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            load8<TI>(src + 8 * q, a);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[8 * q + j] = a[j];
-        }
-    }
     float hi[16], lo[16];
     if (p.norm) {
         double ss = 0.0;
@@ -262,12 +299,20 @@ append_rope_kernel(AppendParams p) {
         for (int j = 0; j < 16; ++j) ss = fma(static_cast<double>(x[j]), static_cast<double>(x[j]), ss);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        const double r = 1.0 / sqrt(ss / D + static_cast<double>(p.eps));
+        const double a = fma(ss, 1.0 / D, static_cast<double>(p.eps));
+        // the fp32 root is good to 2^-22 where fp32 holds `a`; outside, the 64-bit one
+        const float af = static_cast<float>(a);
+        double r;
+        if (af > 1e-30f && af < 1e30f) {
+            const double r0 = static_cast<double>(rsqrtf(af));
+            r = r0 * fma(-0.5 * a * r0, r0, 1.5);
+        } else {
+            r = 1.0 / sqrt(a);
+        }
         const float rh = static_cast<float>(r), rl = static_cast<float>(r - static_cast<double>(rh));
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            const float w = p.weight ? __ldg(p.weight + lane * GROUP + j) : 1.0f;
-            const float ph = w * rh, pl = fmaf(w, rl, fmaf(w, rh, -ph));
+            const float ph = w[j] * rh, pl = fmaf(w[j], rl, fmaf(w[j], rh, -ph));
             const float yh = x[j] * ph, yl = fmaf(x[j], pl, fmaf(x[j], ph, -yh));
             hi[j] = yh + yl;
             lo[j] = yl - (hi[j] - yh);
@@ -281,61 +326,48 @@ append_rope_kernel(AppendParams p) {
     }
 
     uint16_t h[16];
-    const int start = D - p.rope_dim;
-    if (pairs && p.half) {                                  // partners across lanes: by shared memory
-        double* y = reinterpret_cast<double*>(cs + pairs);
+    const int pairs = p.rope_dim / 2, c0 = lane * GROUP - (D - p.rope_dim);    // first channel of the lane among the rotated
 #pragma unroll
-        for (int j = 0; j < 16; ++j) y[lane * GROUP + j] = static_cast<double>(hi[j]) + static_cast<double>(lo[j]);
-    }
-    __syncwarp();
-    if (pairs && lane * GROUP + GROUP > start) {
-        const double* y = reinterpret_cast<const double*>(cs + pairs);
+    for (int j = 0; j < 16; ++j) h[j] = round_bf16(hi[j], lo[j]);
+    if (pairs) {
+        AppendSmem& sm = ar_smem[warp];
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            const int k = lane * GROUP + j - start;        // even: start is even
-            if (k < 0) {
-                h[j] = round_bf16(hi[j], lo[j]);
-                h[j + 1] = round_bf16(hi[j + 1], lo[j + 1]);
-            } else if (!p.half) {
-                const double u = static_cast<double>(hi[j]) + static_cast<double>(lo[j]);
-                const double v = static_cast<double>(hi[j + 1]) + static_cast<double>(lo[j + 1]);
-                const double2 a = cs[k >> 1];
-                h[j] = f64_to_bf16_rne(u * a.x - v * a.y);
-                h[j + 1] = f64_to_bf16_rne(v * a.x + u * a.y);
-            } else {
-#pragma unroll
-                for (int d = 0; d < 2; ++d) {
-                    const int kk = k + d;
-                    const bool second = kk >= pairs;
-                    const double2 a = cs[second ? kk - pairs : kk];
-                    const double me = y[start + kk], other = y[start + (second ? kk - pairs : kk + pairs)];
-                    h[j + d] = f64_to_bf16_rne(second ? me * a.x + other * a.y : me * a.x - other * a.y);
-                }
-            }
+        for (int j = 0; j < 16; ++j)
+            if (c0 + j >= 0) sm.y[c0 + j] = make_float2(hi[j], lo[j]);
+        __syncwarp();
+        for (int k = lane; k < pairs; k += 32) {
+            const int iu = p.half ? k : 2 * k, iv = p.half ? k + pairs : 2 * k + 1;
+            const float2 uf = sm.y[iu], vf = sm.y[iv];
+            const double2 a = turn_cos_sin(turn_fraction(pos, p.inv_freq[k]));
+            const double u = static_cast<double>(uf.x) + static_cast<double>(uf.y);
+            const double v = static_cast<double>(vf.x) + static_cast<double>(vf.y);
+            sm.h[iu] = f64_to_bf16_rne(fma(u, a.x, -(v * a.y)));
+            sm.h[iv] = f64_to_bf16_rne(fma(v, a.x, u * a.y));
         }
-    } else {
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) h[j] = round_bf16(hi[j], lo[j]);
+        for (int j = 0; j < 16; ++j)
+            if (c0 + j >= 0) h[j] = sm.h[c0 + j];
     }
     uint2 v;
-    const uint8_t sc = nvfp4_group(h, v);
+    const uint8_t sc = nvfp4_group_hw(h, v);
     *reinterpret_cast<uint2*>(p.codes + row * ROW_CODES + lane * 8) = v;
     p.scales[row * ROW_SCALES + lane] = sc;
 
     if (!p.idx_proj) return;
     // indexer row: lane l holds values 2l, 2l+1 (a pair of the interleaved rotation)
     float2 k = *reinterpret_cast<const float2*>(p.idx_proj + i * p.idx_stride + 2 * lane);
-    const int ip = p.idx_rope_dim / 2, c0 = 2 * lane - (IDX_DIM - p.idx_rope_dim);
+    const int ip = p.idx_rope_dim / 2, k0 = 2 * lane - (IDX_DIM - p.idx_rope_dim);
     if (ip) {
         if (!p.half) {
             float s = 0.0f, c = 1.0f;
-            if (c0 >= 0) sincospif(2.0f * static_cast<float>(turn_fraction(pos, p.idx_inv_freq[c0 >> 1])), &s, &c);
+            if (k0 >= 0) sincospif(2.0f * static_cast<float>(turn_fraction(pos, p.idx_inv_freq[k0 >> 1])), &s, &c);
             k = make_float2(k.x * c - k.y * s, k.y * c + k.x * s);
         } else {
             float out[2];
 #pragma unroll
             for (int d = 0; d < 2; ++d) {
-                const int kk = c0 + d;
+                const int kk = k0 + d;
                 const bool second = kk >= ip;
                 const int partner = (IDX_DIM - p.idx_rope_dim) + (kk < 0 ? 0 : second ? kk - ip : kk + ip);
                 const float o0 = __shfl_sync(0xFFFFFFFFu, k.x, partner >> 1);
@@ -350,15 +382,14 @@ append_rope_kernel(AppendParams p) {
             k = make_float2(out[0], out[1]);
         }
     }
-    const float2 kr = k;
-    store_idx_row(kr, lane, p.idx_k + row * IDX_DIM, p.idx_kscale + row);
+    store_idx_row(k, lane, p.idx_k + row * IDX_DIM, p.idx_kscale + row);
 }
 
 template <int TI, int TO, int ITEMS>
 csa2_status launch_norm(const RopeParams& p, int rows_per_block, int lanes, int smem, cudaStream_t stream) {
     const unsigned grid = static_cast<unsigned>(ceil_div(p.rows, rows_per_block));
-    if (p.half) norm_rope_kernel<TI, TO, ITEMS, true><<<grid, NR_THREADS, smem, stream>>>(p, rows_per_block, lanes);
-    else norm_rope_kernel<TI, TO, ITEMS, false><<<grid, NR_THREADS, smem, stream>>>(p, rows_per_block, lanes);
+    if (p.half) launch_dependent(norm_rope_kernel<TI, TO, ITEMS, true>, grid, NR_THREADS, smem, stream, p, rows_per_block, lanes);
+    else launch_dependent(norm_rope_kernel<TI, TO, ITEMS, false>, grid, NR_THREADS, smem, stream, p, rows_per_block, lanes);
     return check_launch("norm_rope_kernel");
 }
 
@@ -396,17 +427,13 @@ csa2_status launch_norm_rope(const RopeParams& p, int in_type, int out_type, cud
 
 csa2_status launch_append_rope(const AppendParams& p, int in_type, cudaStream_t stream) {
     if (p.n == 0) return CSA2_OK;
-    const int pairs = p.rope_dim / 2;
-    const int smem = AR_WARPS * (pairs + (p.half && pairs ? D / 2 : 0)) * static_cast<int>(sizeof(double2));
+    const int smem = p.rope_dim ? AR_WARPS * static_cast<int>(sizeof(AppendSmem)) : 0;      // 40 KB
     const int64_t grid = ceil_div(p.n, AR_WARPS);
     if (grid > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
-    const void* fn = in_type == CSA2_T_BF16  ? reinterpret_cast<const void*>(append_rope_kernel<CSA2_T_BF16>)
-                     : in_type == CSA2_T_F16 ? reinterpret_cast<const void*>(append_rope_kernel<CSA2_T_F16>)
-                                             : reinterpret_cast<const void*>(append_rope_kernel<CSA2_T_F32>);
-    constexpr int MAX_SMEM = AR_WARPS * (D / 2 + D / 2) * static_cast<int>(sizeof(double2));
-    if (smem > 48 * 1024 && !opt_in_smem(fn, MAX_SMEM)) return check_launch("append_rope_kernel smem attribute");
-    void* args[] = {const_cast<AppendParams*>(&p)};
-    cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(32 * AR_WARPS), args, smem, stream);
+    const unsigned g = static_cast<unsigned>(grid);
+    if (in_type == CSA2_T_BF16) launch_dependent(append_rope_kernel<CSA2_T_BF16>, g, 32 * AR_WARPS, smem, stream, p);
+    else if (in_type == CSA2_T_F16) launch_dependent(append_rope_kernel<CSA2_T_F16>, g, 32 * AR_WARPS, smem, stream, p);
+    else launch_dependent(append_rope_kernel<CSA2_T_F32>, g, 32 * AR_WARPS, smem, stream, p);
     return check_launch("append_rope_kernel");
 }
 

@@ -15,6 +15,36 @@ __device__ __forceinline__ uint16_t f64_to_bf16_rne(double m) {
     return *reinterpret_cast<uint16_t*>(&h);
 }
 
+// nvfp4_group with the hardware's E2M1 rounding (to nearest even, saturating, the sign kept
+// when the magnitude rounds to 0) and a quotient by reciprocal and one residual step: x and s
+// carry at most 8 and 4 significant bits, so x / s is a rounding midpoint of E2M1 exactly or
+// at least 2^-12 away from it.  The residual x - y s is exact in the fma and brings y to
+// within a unit of the quotient, and to the quotient itself where that has 3 bits.
+__device__ __forceinline__ uint8_t nvfp4_group_hw(const uint16_t (&h)[16], uint2& codes) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, static_cast<uint32_t>(h[i] & 0x7FFFu));
+    const uint8_t scale_code = e4m3_encode_rne_sat(bf16_bits_to_float(static_cast<uint16_t>(top)) / 6.0f);
+    const float s = e4m3_to_float(scale_code), r = scale_code ? 1.0f / s : 0.0f;
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        float y[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float x = bf16_bits_to_float(h[i + e]), y0 = x * r;
+            // (the residual of -0 is +0, which would take its sign)
+            y[e] = __uint_as_float(__float_as_uint(fmaf(fmaf(-y0, s, x), r, y0)) | (static_cast<uint32_t>(h[i + e] & 0x8000u) << 16));
+        }
+        uint32_t b;
+        asm("{ .reg .b8 t; cvt.rn.satfinite.e2m1x2.f32 t, %1, %2; cvt.u32.u8 %0, t; }" : "=r"(b) : "f"(y[1]), "f"(y[0]));
+        w[i / 8] |= b << (4 * (i & 7));
+    }
+    codes.x = w[0];
+    codes.y = w[1];
+    return scale_code;
+}
+
 // Indexer-K row of a position, whole warp: lane l holds values 2l, 2l+1.  kscale = amax /
 // 448 and code = sign | E4M3 RNE saturating of |k / kscale|, both quotients IEEE fp32; an
 // all-zero row gets kscale 0 and zero codes.

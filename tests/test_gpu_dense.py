@@ -215,6 +215,27 @@ def test_append_rope_is_append_kv_without_norm_and_rotation(csa2):
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+def test_append_rope_rounds_like_the_quantiser_everywhere(csa2):
+    """Rows of every bf16 value beside scales of every size: ties, saturation, subnormal and zero
+    scales, signs of zero."""
+    bits = torch.arange(1 << 16, dtype=torch.int32, device=DEV).to(torch.int16).view(BF)
+    bits = bits[bits.isfinite()]
+    bits = torch.cat([bits, bits[: (-bits.numel()) % 512]])
+    rows = [bits.view(-1, 512)]
+    tops = 2.0 ** torch.arange(-12, 12, device=DEV).double()[:, None] * (1 + torch.arange(0, 128, device=DEV).double() / 128)[None]
+    half = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, -0.25, -0.75, -1.25, -1.75, -2.5, -3.5, -5.0, 0.0], device=DEV).double()
+    t = tops.reshape(-1)
+    s = (t / 6).float().clamp(max=448).to(torch.float8_e4m3fn).double()
+    rows.append(torch.cat([t[:, None], half * s[:, None]], 1).to(BF).view(-1, 512))
+    x = torch.cat(rows)
+    n = x.shape[0]
+    a, b = blank_cache(n), blank_cache(n)
+    csa2.quantize_kv(x, 1, a[0], a[1])
+    csa2.append_rope(csa2.append_args(latent=x, pos=torch.arange(n, device=DEV), seq=torch.zeros(n, dtype=torch.int32, device=DEV),
+                                      codes=b[0], scales=b[1], kv_offsets=torch.tensor([0, n], device=DEV), norm=False))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_append_rope_skips_and_reports_what_lies_outside(csa2):
     lat = torch.randn(6, 512, generator=gen(8), device=DEV).to(BF)
     table = torch.tensor([[0, 1], [2, 9], [-1, 3]], dtype=torch.int32, device=DEV)     # page 9 of 4, page -1
