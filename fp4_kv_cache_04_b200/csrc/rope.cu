@@ -196,15 +196,6 @@ norm_rope_kernel(RopeParams p, int rows_per_block, int lanes) {
 
 // ------------------------------------------------------------------ append
 
-// bf16 bits of hi + lo, |lo| <= half a unit of hi, rounded to nearest even: a bf16
-// rounding boundary is an fp32 number, so only hi exactly on it needs lo's sign.
-__device__ __forceinline__ uint16_t round_bf16(float hi, float lo) {
-    uint32_t b = __float_as_uint(hi);
-    if ((b & 0xFFFFu) == 0x8000u && lo != 0.0f) b += (lo > 0.0f) == (hi > 0.0f) ? 1u : 0xFFFFFFFFu;
-    const __nv_bfloat16 h = __float2bfloat16_rn(__uint_as_float(b));
-    return *reinterpret_cast<const uint16_t*>(&h);
-}
-
 // sin and cos of 2 pi t, |t| <= 1/2, in 64 bits: the nearest quarter turn taken off leaves
 // |x| <= pi/4, where the Taylor series to x^13 and x^14 are off by less than 2^-45.
 __device__ __forceinline__ double2 turn_cos_sin(double t) {
@@ -231,20 +222,24 @@ __device__ __forceinline__ double2 turn_cos_sin(double t) {
 
 constexpr int AR_WARPS = 8;
 
-struct AppendSmem {
-    float2 y[D];                               // normed channels as hi + lo, the rotated ones only
-    uint16_t h[D];                             // those turned and rounded to bf16
-};
+template <int T>
+__device__ __forceinline__ float load1(const typename Elem<T>::type* p) {
+    if constexpr (T == CSA2_T_BF16) return __bfloat162float(*p);
+    else if constexpr (T == CSA2_T_F16) return __half2float(*p);
+    else return *p;
+}
 
 // One warp per token, one lane per 16-channel group (as in quantize.cu).  The FP4 codes
 // change by a whole step at a border, so the bf16 value they are made of is the real
 // number's rounding: the sum of squares in 64 bits, 1/sqrt by one 64-bit Newton step from
-// the fp32 one (2^-43), x * (w * r) as an fp32 pair hi + lo (its error ~2^-45), the rotated
-// channels in 64 bits, a pair per lane and turn, exchanged through shared memory.
+// the fp32 one (2^-43); x * w * r in fp32 (off by 3 units at most), and again in 64 bits by
+// the whole warp where one of its 512 results lies within 4 units of a bf16 rounding border
+// (1 token in 14); the rotated channels in 64 bits throughout, a pair per lane and turn,
+// handed to their group's lane through shared memory.
 template <int TI>
 __global__ void __launch_bounds__(32 * AR_WARPS)
 append_rope_kernel(AppendParams p) {
-    extern __shared__ AppendSmem ar_smem[];
+    extern __shared__ uint16_t ar_smem[];                   // [warps][rope_dim rounded up to 8]: turned channels, bf16
     griddep_launch_dependents();
     griddep_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -279,8 +274,11 @@ append_rope_kernel(AppendParams p) {
     if (b >= 0 && b < p.batch) {
         if (p.rows.page_table) {
             if (pos < static_cast<int64_t>(p.rows.pages_per_seq) * p.rows.page_rows) {
-                const int64_t pg = p.rows.page_table[b * p.rows.pages_per_seq + pos / p.rows.page_rows];
-                if (pg >= 0) row = pg * p.rows.page_rows + pos % p.rows.page_rows;
+                // 32-bit division wherever the position fits
+                const int64_t in_seq = pos >> 32 ? pos / p.rows.page_rows
+                                                 : static_cast<int64_t>(static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.rows.page_rows));
+                const int64_t pg = p.rows.page_table[b * p.rows.pages_per_seq + in_seq];
+                if (pg >= 0) row = pg * p.rows.page_rows + (pos - in_seq * p.rows.page_rows);
             }
         } else {
             const int64_t o = p.kv_offsets[b];
@@ -292,7 +290,7 @@ append_rope_kernel(AppendParams p) {
         return;
     }
 
-    float hi[16], lo[16];
+    double r = 1.0;
     if (p.norm) {
         double ss = 0.0;
 #pragma unroll
@@ -302,52 +300,60 @@ append_rope_kernel(AppendParams p) {
         const double a = fma(ss, 1.0 / D, static_cast<double>(p.eps));
         // the fp32 root is good to 2^-22 where fp32 holds `a`; outside, the 64-bit one
         const float af = static_cast<float>(a);
-        double r;
         if (af > 1e-30f && af < 1e30f) {
             const double r0 = static_cast<double>(rsqrtf(af));
             r = r0 * fma(-0.5 * a * r0, r0, 1.5);
         } else {
             r = 1.0 / sqrt(a);
         }
-        const float rh = static_cast<float>(r), rl = static_cast<float>(r - static_cast<double>(rh));
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float ph = w[j] * rh, pl = fmaf(w[j], rl, fmaf(w[j], rh, -ph));
-            const float yh = x[j] * ph, yl = fmaf(x[j], pl, fmaf(x[j], ph, -yh));
-            hi[j] = yh + yl;
-            lo[j] = yl - (hi[j] - yh);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            hi[j] = x[j];
-            lo[j] = 0.0f;
-        }
     }
 
     uint16_t h[16];
-    const int pairs = p.rope_dim / 2, c0 = lane * GROUP - (D - p.rope_dim);    // first channel of the lane among the rotated
+    {
+        const float rf = static_cast<float>(r);
+        float y[16];
+        bool close = false;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) h[j] = round_bf16(hi[j], lo[j]);
-    if (pairs) {
-        AppendSmem& sm = ar_smem[warp];
+        for (int j = 0; j < 16; ++j) {
+            y[j] = x[j] * (w[j] * rf);
+            close |= ((__float_as_uint(y[j]) - 0x7FFCu) & 0xFFFFu) <= 8u;
+        }
+        if (p.norm && __any_sync(0xFFFFFFFFu, close)) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (c0 + j >= 0) sm.y[c0 + j] = make_float2(hi[j], lo[j]);
-        __syncwarp();
+            for (int j = 0; j < 16; ++j)
+                h[j] = f64_to_bf16_rne(static_cast<double>(x[j]) * (static_cast<double>(w[j]) * r));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                const __nv_bfloat162 two = __floats2bfloat162_rn(y[j], y[j + 1]);
+                const uint32_t u = *reinterpret_cast<const uint32_t*>(&two);
+                h[j] = static_cast<uint16_t>(u);
+                h[j + 1] = static_cast<uint16_t>(u >> 16);
+            }
+        }
+    }
+    if (p.rope_dim) {
+        const int pairs = p.rope_dim / 2, start = D - p.rope_dim;
+        uint16_t* turned = ar_smem + warp * ((p.rope_dim + 7) & ~7);
+        const auto* xr = static_cast<const typename Elem<TI>::type*>(p.latent) + i * p.latent_stride + start;
         for (int k = lane; k < pairs; k += 32) {
             const int iu = p.half ? k : 2 * k, iv = p.half ? k + pairs : 2 * k + 1;
-            const float2 uf = sm.y[iu], vf = sm.y[iv];
             const double2 a = turn_cos_sin(turn_fraction(pos, p.inv_freq[k]));
-            const double u = static_cast<double>(uf.x) + static_cast<double>(uf.y);
-            const double v = static_cast<double>(vf.x) + static_cast<double>(vf.y);
-            sm.h[iu] = f64_to_bf16_rne(fma(u, a.x, -(v * a.y)));
-            sm.h[iv] = f64_to_bf16_rne(fma(v, a.x, u * a.y));
+            double u = static_cast<double>(load1<TI>(xr + iu)), v = static_cast<double>(load1<TI>(xr + iv));
+            if (p.norm) {
+                u *= p.weight ? static_cast<double>(p.weight[start + iu]) * r : r;
+                v *= p.weight ? static_cast<double>(p.weight[start + iv]) * r : r;
+            }
+            turned[iu] = f64_to_bf16_rne(fma(u, a.x, -(v * a.y)));
+            turned[iv] = f64_to_bf16_rne(fma(v, a.x, u * a.y));
         }
         __syncwarp();
+        const int c0 = lane * GROUP - start;                // first channel of the lane among the rotated
+        if (c0 + GROUP > 0) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (c0 + j >= 0) h[j] = sm.h[c0 + j];
+            for (int j = 0; j < 16; ++j)
+                if (c0 + j >= 0) h[j] = turned[c0 + j];
+        }
     }
     uint2 v;
     const uint8_t sc = nvfp4_group_hw(h, v);
@@ -427,7 +433,7 @@ csa2_status launch_norm_rope(const RopeParams& p, int in_type, int out_type, cud
 
 csa2_status launch_append_rope(const AppendParams& p, int in_type, cudaStream_t stream) {
     if (p.n == 0) return CSA2_OK;
-    const int smem = p.rope_dim ? AR_WARPS * static_cast<int>(sizeof(AppendSmem)) : 0;      // 40 KB
+    const int smem = AR_WARPS * ((p.rope_dim + 7) & ~7) * 2;
     const int64_t grid = ceil_div(p.n, AR_WARPS);
     if (grid > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
     const unsigned g = static_cast<unsigned>(grid);

@@ -15,6 +15,13 @@ __device__ __forceinline__ uint16_t f64_to_bf16_rne(double m) {
     return *reinterpret_cast<uint16_t*>(&h);
 }
 
+// E4M3 codes of lo (bits 0..7) and hi (8..15), to nearest even, saturating at 448.
+__device__ __forceinline__ uint32_t e4m3x2_rn(float lo, float hi) {
+    uint16_t v;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
+    return v;
+}
+
 // nvfp4_group with the hardware's E2M1 rounding (to nearest even, saturating, the sign kept
 // when the magnitude rounds to 0) and a quotient by reciprocal and one residual step: x and s
 // carry at most 8 and 4 significant bits, so x / s is a rounding midpoint of E2M1 exactly or
@@ -24,8 +31,11 @@ __device__ __forceinline__ uint8_t nvfp4_group_hw(const uint16_t (&h)[16], uint2
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = max(top, static_cast<uint32_t>(h[i] & 0x7FFFu));
-    const uint8_t scale_code = e4m3_encode_rne_sat(bf16_bits_to_float(static_cast<uint16_t>(top)) / 6.0f);
-    const float s = e4m3_to_float(scale_code), r = scale_code ? 1.0f / s : 0.0f;
+    // amax / 6 by the same two steps: 8 bits over 2, against E4M3's midpoints of 5
+    const float amax = bf16_bits_to_float(static_cast<uint16_t>(top)), q0 = amax * (1.0f / 6.0f);
+    const uint32_t scale_code = e4m3x2_rn(fmaf(fmaf(-q0, 6.0f, amax), 1.0f / 6.0f, q0), 0.0f) & 0xFFu;
+    const float s = e4m3_to_float(static_cast<uint8_t>(scale_code));
+    const float r = scale_code ? __frcp_rn(s) : 0.0f;
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
@@ -42,7 +52,7 @@ __device__ __forceinline__ uint8_t nvfp4_group_hw(const uint16_t (&h)[16], uint2
     }
     codes.x = w[0];
     codes.y = w[1];
-    return scale_code;
+    return static_cast<uint8_t>(scale_code);
 }
 
 // Indexer-K row of a position, whole warp: lane l holds values 2l, 2l+1.  kscale = amax /
@@ -53,13 +63,8 @@ __device__ __forceinline__ void store_idx_row(float2 k, int lane, uint8_t* idx_k
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
     const float ks = amax / 448.0f;
-    uint32_t c0 = 0, c1 = 0;
-    if (ks > 0.0f) {
-        const float q0 = k.x / ks, q1 = k.y / ks;
-        c0 = (signbit(q0) ? 0x80u : 0u) | e4m3_encode_rne_sat(fabsf(q0));
-        c1 = (signbit(q1) ? 0x80u : 0u) | e4m3_encode_rne_sat(fabsf(q1));
-    }
-    reinterpret_cast<uint16_t*>(idx_k)[lane] = static_cast<uint16_t>(c0 | (c1 << 8));
+    const uint32_t c = ks > 0.0f ? e4m3x2_rn(k.x / ks, k.y / ks) : 0u;
+    reinterpret_cast<uint16_t*>(idx_k)[lane] = static_cast<uint16_t>(c);
     if (lane == 0) *idx_kscale = ks;
 }
 
