@@ -709,10 +709,10 @@ csa2_status csa2_attend_cache(const csa2_cache_args* a, void* stream) {
     p.q_per_seq = a->q_per_seq;
     p.ratio = a->ratio;
     p.out_f32 = a->out_type == CSA2_T_F32;
-    p.max_n = a->max_n;
-    p.total_n = a->total_n;
-    p.window = a->window;
-    p.sinks = a->sinks;
+    p.max_n = static_cast<int>(a->max_n);
+    p.total_n = static_cast<int>(a->total_n);
+    p.window = static_cast<int>(std::min<int64_t>(a->window, INT32_MAX));
+    p.sinks = static_cast<int>(std::min<int64_t>(a->sinks, INT32_MAX));
     p.kv_offsets = a->kv_offsets;
     p.q_pos = a->q_pos;
     p.codes = a->codes;

@@ -25,21 +25,18 @@ struct RowView {
 };
 
 __device__ __forceinline__ RowView row_view(const CacheParams& p, int row) {
-    const int b = row / p.q_per_seq;
-    int64_t n = p.kv_offsets[b + 1] - p.kv_offsets[b];
-    n = max(static_cast<int64_t>(0), min(n, p.max_n));
+    const int b = p.q_per_seq == 1 ? row : row / p.q_per_seq;
+    int n = static_cast<int>(max(static_cast<int64_t>(0), min(p.kv_offsets[b + 1] - p.kv_offsets[b], static_cast<int64_t>(p.max_n))));
     if (p.q_pos) {
         const int64_t t = p.q_pos[b] + (row - b * p.q_per_seq) + 1;
-        n = min(n, max(static_cast<int64_t>(0), t / p.ratio));
+        n = static_cast<int>(min(static_cast<int64_t>(n), max(static_cast<int64_t>(0), t) >> (p.ratio - 1)));
     }
     RowView v;
-    v.n_vis = static_cast<int>(n);
-    const int64_t w = p.window > 0 ? max(static_cast<int64_t>(0), n - p.window) : 0;
-    v.w_beg = static_cast<int>(w);
-    const int64_t s = p.window > 0 ? min(p.sinks, n) : 0;
-    v.w0 = static_cast<int>(w / CACHE_TILE);
-    v.ts = static_cast<int>(min(ceil_div(s, CACHE_TILE), static_cast<int64_t>(v.w0)));
-    v.tiles = n > 0 ? v.ts + static_cast<int>(ceil_div(n, CACHE_TILE)) - v.w0 : 0;
+    v.n_vis = n;
+    v.w_beg = p.window > 0 ? max(0, n - p.window) : 0;
+    v.w0 = v.w_beg / CACHE_TILE;
+    v.ts = p.window > 0 ? min((min(p.sinks, n) + CACHE_TILE - 1) / CACHE_TILE, v.w0) : 0;
+    v.tiles = n > 0 ? v.ts + (n + CACHE_TILE - 1) / CACHE_TILE - v.w0 : 0;
     return v;
 }
 
@@ -53,69 +50,64 @@ struct Range {
     int row, tile, count;
 };
 
-// Sum of v over the block, and the sum of the threads before this one.  red: 32 words.
+// Each warp sums an equal share of the rows; the share, then the row, in which the range
+// starts is found from those sums.  red: 34 words.
 template <int THREADS>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t& before, int64_t* red) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    int64_t inc = v;
+__device__ __forceinline__ Range my_range(const CacheParams& p, int (&red)[34]) {
+    constexpr int WARPS = THREADS / 32;
+    static_assert(WARPS <= 32, "one lane per warp");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, c = blockIdx.x;
+    int lo = 0, hi = p.batch * p.q_per_seq;
+    if (p.whole_rows) {                                     // rows dealt out uncut
+        const int each = hi / p.ranges, more = hi % p.ranges;
+        lo = c * each + min(c, more);
+        hi = lo + each + (c < more ? 1 : 0);
+    }
+    const int share = (hi - lo + WARPS - 1) / WARPS, r0 = lo + warp * share, r1 = min(hi, r0 + share);
+    int sum = 0;
+    for (int r = r0 + lane; r < r1; r += 32) sum += row_view(p, r).tiles;
+    sum = __reduce_add_sync(0xFFFFFFFFu, sum);
+    if (lane == 0) red[warp] = sum;
+    __syncthreads();
+    const int mine = lane < WARPS ? red[lane] : 0;
+    int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += u;
+        const int u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += u;
     }
-    if (lane == 31) red[warp] = inc;
-    __syncthreads();
-    int64_t all = 0;
-    before = inc - v;
+    const int total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    int t0 = 0, count = total;
+    if (!p.whole_rows) {
+        // with fewer tiles than ranges the first `total` ranges take one each: a cut row's
+        // ranges are always consecutive
+        const int g = max(1, min(p.ranges, total)), each = total / g, more = total % g;
+        t0 = c * each + min(c, more);
+        count = c < g ? each + (c < more ? 1 : 0) : 0;
+    }
+    if (count == 0 || total == 0) return Range{0, 0, 0};
+    const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, upto > t0)) - 1;
+    if (warp == owner) {
+        int before = __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
+        for (int r = r0; r < r1; r += 32) {
+            const int n = r + lane < r1 ? row_view(p, r + lane).tiles : 0;
+            int inc = n;
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) before += red[w];
-        all += red[w];
+            for (int o = 1; o < 32; o *= 2) {
+                const int u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                if (lane >= o) inc += u;
+            }
+            const int first = before + inc - n;
+            if (n > 0 && t0 >= first && t0 < first + n) {
+                red[32] = r + lane;
+                red[33] = t0 - first;
+            }
+            before += __shfl_sync(0xFFFFFFFFu, inc, 31);
+            if (before > t0) break;
+        }
     }
     __syncthreads();
-    return all;
-}
-
-template <int THREADS>
-__device__ __forceinline__ Range my_range(const CacheParams& p, int64_t (&red)[34]) {
-    const int64_t rows = static_cast<int64_t>(p.batch) * p.q_per_seq;
-    const int64_t c = blockIdx.x;
-    int64_t before;
-    if (p.whole_rows) {                                     // rows dealt out uncut
-        const int64_t r0 = rows * c / p.ranges, r1 = rows * (c + 1) / p.ranges;
-        int64_t sum = 0;
-        for (int64_t r = r0 + threadIdx.x; r < r1; r += THREADS) sum += row_view(p, static_cast<int>(r)).tiles;
-        return Range{static_cast<int>(r0), 0, static_cast<int>(block_scan<THREADS>(sum, before, red))};
-    }
-    // one pass over the rows finds the total, a second one (none for THREADS rows or fewer)
-    // the row in which this range starts
-    int mine = threadIdx.x < rows ? row_view(p, threadIdx.x).tiles : 0;
-    int64_t sum = mine;
-    for (int64_t r = threadIdx.x + THREADS; r < rows; r += THREADS) sum += row_view(p, static_cast<int>(r)).tiles;
-    const int64_t total = block_scan<THREADS>(sum, before, red);
-    // with fewer tiles than ranges the first `total` ranges take one each: a cut row's
-    // ranges are always consecutive
-    const int64_t g = min(static_cast<int64_t>(p.ranges), total);
-    if (c >= g) return Range{0, 0, 0};
-    const int64_t t0 = total * c / g, t1 = total * (c + 1) / g;
-    if (threadIdx.x == 0) red[32] = -1;
-    int64_t base = 0;
-    for (int64_t r0 = 0; r0 < rows; r0 += THREADS) {
-        const int64_t r = r0 + threadIdx.x;
-        if (r0 > 0) mine = r < rows ? row_view(p, r).tiles : 0;
-        int64_t first = before, all = total;
-        if (rows > THREADS) all = block_scan<THREADS>(mine, first, red);
-        else __syncthreads();
-        first += base;
-        if (mine > 0 && t0 >= first && t0 < first + mine) {
-            red[32] = r;
-            red[33] = t0 - first;
-        }
-        base += all;
-        __syncthreads();
-        if (red[32] >= 0) break;
-    }
-    return Range{static_cast<int>(red[32]), static_cast<int>(red[33]), static_cast<int>(t1 - t0)};
+    return Range{red[32], red[33], count};
 }
 
 // Rows that see nothing: zeros, lse -inf.  One warp of each CTA; CTA c looks at rows 32 c ..
@@ -172,7 +164,7 @@ struct alignas(1024) CacheSmem {
     alignas(16) float ref[2][HEADS], part_m[4][HEADS];
     int issued[AC_STAGES];                         // copies issued into each stage
     uint32_t tmem;
-    int64_t red[34];
+    int red[34];
 };
 static_assert(sizeof(CacheSmem) + 1024 <= 232448, "shared memory of one SM");
 
@@ -258,6 +250,17 @@ __device__ __forceinline__ void scale_heads(const uint64_t (&s)[HEADS / 2], cons
         const float2 a = unpack2(fma2(s[2 * i], fv.x, cv.x)), b = unpack2(fma2(s[2 * i + 1], fv.y, cv.y));
         x[4 * i] = a.x, x[4 * i + 1] = a.y, x[4 * i + 2] = b.x, x[4 * i + 3] = b.y;
     }
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // Next row at or after `row` that sees anything (whole warp; there is one).
@@ -431,7 +434,6 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
     // every role walks the range's rows by itself: it counts tiles, rw rows
     int it = 0, rw = 0;
     int row = range.row, left = range.count, tile = range.tile;
-    if (left > 0) row = next_row(p, row);
 
     if (warp == AC_TMA_WARP) {
         // ---- producer: runs ahead over the rows, AC_STAGES tiles at most
@@ -686,8 +688,16 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
             // converts channels 8 g .. + 7 of those (half a scale group) of the keys of its B
             // fragments, n-tile i being channel i of every such half group
             const int wd = warp & 7, kh = warp >> 3, g = lane >> 2, t4 = lane & 3;
-            const uint32_t code_off = (wd >> 2) * (AC_CODE_BYTES / 2) + (g & 3) * 4;
-            const uint32_t chunk = (wd & 3) * 2 + (g >> 2);
+            // byte offsets in a stage of the lane's codes of keys 2 t and 2 t + 1 (their swizzles),
+            // and of their scales; in P of the row that the lane hands to ldmatrix
+            const uint32_t code0 = (wd >> 2) * (AC_CODE_BYTES / 2) + (64 * kh + 2 * t4) * 128 + (g & 3) * 4 +
+                                   ((((wd & 3) * 2 + (g >> 2)) ^ (2 * t4)) << 4);
+            const uint32_t code1 = (wd >> 2) * (AC_CODE_BYTES / 2) + (64 * kh + 2 * t4 + 1) * 128 + (g & 3) * 4 +
+                                   ((((wd & 3) * 2 + (g >> 2)) ^ (2 * t4 + 1)) << 4);
+            const uint32_t scale0 = AC_CODE_BYTES + (64 * kh + 2 * t4) * ROW_SCALES + wd * 4 + (g >> 1);
+            const uint32_t stage0 = smem_u32(sm.stage[0]);
+            const uint32_t p0 = smem_u32(sm.p[0]) + (64 * kh + ((lane >> 4) << 3) + (lane & 7)) * 32 +
+                                ((((lane >> 3) ^ (lane >> 2)) & 1) << 4);
             while (left > 0) {
                 if (rw > 0) row = next_row(p, row);
                 const int tiles = row_view(p, row).tiles;
@@ -698,21 +708,21 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                 for (int t = tile; t < end; ++t, ++it) {
                     const int st = it % AC_STAGES, buf = it & 1;
                     if (!ready) wait(&sm.p_full[buf], it >> 1);
-                    const uint8_t* codes = sm.stage[st] + code_off;
-                    const uint8_t* scales = sm.stage[st] + AC_CODE_BYTES + wd * 4 + (g >> 1);
-                    const uint32_t pa = smem_u32(sm.p[buf]);
+                    const uint32_t sa = stage0 + st * AC_STAGE_BYTES, ca0 = sa + code0, ca1 = sa + code1, xa = sa + scale0;
+                    const uint32_t pa = p0 + buf * AC_P_BYTES;
                     // step ks + 1's operands are loaded while step ks is multiplied
                     uint32_t a[2][4], c[2][4], sc[2][4];
-                    auto load_step = [&](int ks) {
-                        const int kb = 64 * kh + 16 * ks, n = ks & 1;
-                        const int ak = kb + ((lane >> 4) << 3) + (lane & 7);
-                        ldmatrix_x4_trans(a[n], pa + ak * 32 + ((((lane >> 3) ^ (ak >> 2)) & 1) << 4));
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int key = kb + 2 * t4 + (j & 1) + 8 * (j >> 1);
-                            c[n][j] = *reinterpret_cast<const uint32_t*>(codes + key * 128 + ((chunk ^ (key & 7)) << 4));
-                            sc[n][j] = scales[key * ROW_SCALES];
-                        }
+                    auto load_step = [&](int ks) {           // keys 16 ks + 2 t + {0, 1, 8, 9}
+                        const int n = ks & 1;
+                        ldmatrix_x4_trans(a[n], pa + ks * 16 * 32);
+                        c[n][0] = lds32(ca0 + ks * 2048);
+                        c[n][1] = lds32(ca1 + ks * 2048);
+                        c[n][2] = lds32(ca0 + ks * 2048 + 1024);
+                        c[n][3] = lds32(ca1 + ks * 2048 + 1024);
+                        sc[n][0] = lds8(xa + ks * 512);
+                        sc[n][1] = lds8(xa + ks * 512 + 32);
+                        sc[n][2] = lds8(xa + ks * 512 + 256);
+                        sc[n][3] = lds8(xa + ks * 512 + 288);
                     };
                     load_step(0);
                     const float n0 = sm.ref[buf][g], n1 = sm.ref[buf][g + 8];
@@ -733,8 +743,8 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         const int n = ks & 1;
                         if (ks < 3) load_step(ks + 1);
                         else ready = t + 1 < end ? poll(&sm.p_full[buf ^ 1], (it + 1) >> 1) : 0u;
-                        const uint32_t s0 = e4m3x2_to_f16x2(static_cast<uint16_t>(sc[n][0] | (sc[n][1] << 8)));
-                        const uint32_t s1 = e4m3x2_to_f16x2(static_cast<uint16_t>(sc[n][2] | (sc[n][3] << 8)));
+                        const uint32_t s0 = e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(sc[n][0], sc[n][1], 0x40)));
+                        const uint32_t s1 = e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(sc[n][2], sc[n][3], 0x40)));
                         // two keys' codes interleaved: byte i of ev / od = channel 2 i / 2 i + 1 of both
                         uint32_t e0[4], e1[4], d0[4], d1[4];
                         e2m1x8_to_f16((c[n][0] & 0x0F0F0F0Fu) | ((c[n][1] << 4) & 0xF0F0F0F0u), e0);

@@ -74,7 +74,8 @@ csa2_status launch_append_rope(const AppendParams& p, int in_type, cudaStream_t 
 // joined from the ranges' partials.
 struct CacheParams {
     int batch, q_per_seq, ratio, out_f32;
-    int64_t max_n, total_n, window, sinks;
+    int max_n, total_n;
+    int window, sinks;        // clamped to 2^31 - 1
     const int64_t* kv_offsets;
     const int64_t* q_pos;
     const uint8_t* codes;
