@@ -162,6 +162,7 @@ struct alignas(1024) CacheSmem {
     // per tile: the reference its P stands at
     alignas(16) float f[2][HEADS], l[2][4][HEADS], minus_m[2][HEADS];
     alignas(16) float ref[2][HEADS], part_m[4][HEADS];
+    int moved[2];
     int issued[AC_STAGES];                         // copies issued into each stage
     uint32_t tmem;
     int red[34];
@@ -202,6 +203,19 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&o)[4]) {
     asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %4; cvt.rn.f16x2.e2m1x2 %0, a; cvt.rn.f16x2.e2m1x2 %1, b; "
         "cvt.rn.f16x2.e2m1x2 %2, c; cvt.rn.f16x2.e2m1x2 %3, d; }"
         : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(w));
+}
+
+// Two E4M3 bytes -> f16x2.
+__device__ __forceinline__ uint32_t scales_to_f16x2(uint32_t two) {
+    uint32_t r;
+    asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(r) : "r"(two));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
@@ -608,12 +622,13 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
 #pragma unroll
                         for (int h = 0; h < HEADS; ++h) x[h] = vis ? x[h] : -INFINITY;
                     }
-                    float d = x[0];
+                    float d = fmaxf(x[0], x[1]);
 #pragma unroll
-                    for (int h = 1; h < HEADS; ++h) d = fmaxf(d, x[h]);
+                    for (int h = 2; h < HEADS; h += 2) d = max3(d, x[h], x[h + 1]);
                     if (it >= 2) wait(&sm.p_empty[buf], (it >> 1) - 1);
                     const bool first = t == tile;
-                    if (vote_barrier(BAR_VOTE, 128, d > AC_GAP + AC_SHIFT || first)) {
+                    const bool moved = vote_barrier(BAR_VOTE, 128, d > AC_GAP + AC_SHIFT || first);
+                    if (moved) {
                         // back to plain logits, their maximum over the tile's keys, and a new reference
 #pragma unroll
                         for (int h = 0; h < HEADS; ++h) x[h] = vis ? x[h] - sm.minus_m[rb][h] : -INFINITY;
@@ -641,7 +656,10 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         if (warp == AC_SM_WARP && lane < HEADS) sm.minus_m[rb][lane] = -mine;
                         named_barrier(BAR_MAX, 128);
                     }
-                    if (warp == AC_SM_WARP && lane < HEADS) sm.ref[buf][lane] = -sm.minus_m[rb][lane];
+                    if (warp == AC_SM_WARP) {                // the warps of P V rescale O where it moved
+                        if (moved && lane < HEADS) sm.ref[buf][lane] = -sm.minus_m[rb][lane];
+                        if (lane == 0) sm.moved[buf] = moved;
+                    }
                     uint32_t pk[HEADS / 2];
 #pragma unroll
                     for (int h = 0; h < HEADS; h += 2) {
@@ -725,9 +743,9 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         sc[n][3] = lds8(xa + ks * 512 + 288);
                     };
                     load_step(0);
-                    const float n0 = sm.ref[buf][g], n1 = sm.ref[buf][g + 8];
-                    if (__any_sync(0xFFFFFFFFu, n0 != m0 || n1 != m1)) {
-                        const float a0 = n0 == m0 ? 1.0f : fast_exp2(m0 - n0), a1 = n1 == m1 ? 1.0f : fast_exp2(m1 - n1);
+                    if (sm.moved[buf]) {
+                        const float n0 = sm.ref[buf][g], n1 = sm.ref[buf][g + 8];
+                        const float a0 = fast_exp2(m0 - n0), a1 = fast_exp2(m1 - n1);
                         m0 = n0;
                         m1 = n1;
 #pragma unroll
@@ -743,8 +761,8 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         const int n = ks & 1;
                         if (ks < 3) load_step(ks + 1);
                         else ready = t + 1 < end ? poll(&sm.p_full[buf ^ 1], (it + 1) >> 1) : 0u;
-                        const uint32_t s0 = e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(sc[n][0], sc[n][1], 0x40)));
-                        const uint32_t s1 = e4m3x2_to_f16x2(static_cast<uint16_t>(__byte_perm(sc[n][2], sc[n][3], 0x40)));
+                        const uint32_t s0 = scales_to_f16x2(__byte_perm(sc[n][0], sc[n][1], 0x40));
+                        const uint32_t s1 = scales_to_f16x2(__byte_perm(sc[n][2], sc[n][3], 0x40));
                         // two keys' codes interleaved: byte i of ev / od = channel 2 i / 2 i + 1 of both
                         uint32_t e0[4], e1[4], d0[4], d1[4];
                         e2m1x8_to_f16((c[n][0] & 0x0F0F0F0Fu) | ((c[n][1] << 4) & 0xF0F0F0F0u), e0);
