@@ -127,11 +127,11 @@ __device__ __forceinline__ void empty_rows(const CacheParams& p) {
 }
 
 // ---------------------------------------------------------------- the kernel
-constexpr int AC_THREADS = 736;
-constexpr int AC_PV_WARPS = 16;                    // warps 0-7, 8-15: P V of a tile's first / last 64 keys
-constexpr int AC_SM_WARP = 16;                     // warps 16-19: softmax (TMEM lane quarters 0-3)
-constexpr int AC_TMA_WARP = 20;
-constexpr int AC_MMA_WARP = 21;                    // warps 21, 22: scales and MMAs of even / odd tiles,
+constexpr int AC_THREADS = 480;
+constexpr int AC_PV_WARPS = 8;                     // warps 0-3, 4-7: P V of a tile's first / last 64 keys
+constexpr int AC_SM_WARP = 8;                      // warps 8-11: softmax (TMEM lane quarters 0-3)
+constexpr int AC_TMA_WARP = 12;
+constexpr int AC_MMA_WARP = 13;                    // warps 13, 14: scales and MMAs of even / odd tiles,
                                                    // and half of the next row's query each
 constexpr int AC_STAGES = 4;
 constexpr int AC_CODE_BYTES = CACHE_TILE * ROW_CODES;                    // two panels of 16 KB
@@ -143,7 +143,7 @@ constexpr int AC_P_BYTES = CACHE_TILE * HEADS * 2;
 // tensor memory: two S accumulators, the tile's scales twice, the digits' scales
 constexpr uint32_t AT_COLS = 512, AT_S = 0, AT_S_STEP = 128, AT_SFA = 256, AT_SFB = 320;
 // named barriers
-constexpr int BAR_VOTE = 1, BAR_MAX = 2, BAR_PV = 3;   // BAR_PV + w: warps w and w + 8
+constexpr int BAR_VOTE = 1, BAR_MAX = 2, BAR_PV = 3;   // BAR_PV + w: warps w and w + 4
 constexpr float AC_GAP = 4.0f;                     // the reference maximum moves by more than 2^4 ...
 constexpr float AC_SHIFT = 11.0f;                  // ... and P is kept times 2^11, at most 2^15 in f16
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
@@ -153,7 +153,7 @@ struct alignas(1024) CacheSmem {
     uint8_t q[2][2 * AC_QPANEL];                   // query digits of two rows, K-major SW128 panels
     uint8_t p[2][AC_P_BYTES];                      // P [key][head] f16
     uint8_t sf[2][8][512];                         // a tile's scales as 32 x 16 B blocks
-    float4 x[AC_PV_WARPS / 2][4][32];              // O passed between the two key halves
+    float4 x[AC_PV_WARPS / 2][8][32];              // O passed between the two key halves
     // tiles: loaded / read, S written / read, P written / read; rows: query written / read,
     // statistics written / read
     uint64_t full[AC_STAGES], empty[AC_STAGES], s_full[2], s_empty[2], p_full[2], p_empty[2];
@@ -266,9 +266,9 @@ __device__ __forceinline__ void scale_heads(const uint64_t (&s)[HEADS / 2], cons
     }
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
@@ -505,9 +505,11 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                 if (sm.issued[st]) mbar_wait(&sm.full[st], static_cast<uint32_t>((sm.issued[st] - 1) & 1), err);
         }
     } else {
-        // the first row's query: a head per P V warp; the following rows' by the MMA warps
-        if (left > 0 && warp < AC_PV_WARPS) {
-            put_query(p, sm, 0, warp, load_query(p, row, warp));
+        // the first row's query: a head or two per P V and softmax warp; the following rows' by the
+        // MMA warps
+        if (left > 0 && warp < AC_TMA_WARP) {
+#pragma unroll 1
+            for (int h = warp; h < HEADS; h += AC_TMA_WARP) put_query(p, sm, 0, h, load_query(p, row, h));
             fence_proxy_async_smem();
         }
         __syncthreads();
@@ -604,13 +606,14 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                     uint64_t s[HEADS / 2];                  // the digits' columns summed, two heads a pair
                     const uint32_t src = tm + (static_cast<uint32_t>(32 * quarter) << 16) + AT_S + AT_S_STEP * buf;
 #pragma unroll
-                    for (int i = 0; i < AC_DIGITS; ++i) {
-                        uint32_t r[HEADS];
-                        tmem_ld16(src + HEADS * i, r);
+                    for (int i = 0; i < AC_DIGITS; i += 2) {
+                        uint32_t r[2 * HEADS];
+                        tmem_ld32(src + HEADS * i, r);
 #pragma unroll
                         for (int h = 0; h < HEADS / 2; ++h) {
-                            const uint64_t one = pack2(__uint_as_float(r[2 * h]), __uint_as_float(r[2 * h + 1]));
-                            s[h] = i ? add2(s[h], one) : one;
+                            const uint64_t two = add2(pack2(__uint_as_float(r[2 * h]), __uint_as_float(r[2 * h + 1])),
+                                                      pack2(__uint_as_float(r[16 + 2 * h]), __uint_as_float(r[17 + 2 * h])));
+                            s[h] = i ? add2(s[h], two) : two;
                         }
                     }
                     tc_fence_before();
@@ -679,7 +682,6 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         z[0] = z[1] = make_uint4(0u, 0u, 0u, 0u);
                         fence_proxy_async_smem();            // before the next copy into this stage
                     }
-                    wait(&sm.full[st], it / AC_STAGES);      // P V reads the tile on this word
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.p_full[buf]);
                 }
@@ -702,17 +704,16 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                 ++rw;
             }
         } else {
-            // ---- P V: warp owns channels 64 (w % 8) .. + 63 of keys 64 (w / 8) .. + 63; lane (g, t)
-            // converts channels 8 g .. + 7 of those (half a scale group) of the keys of its B
-            // fragments, n-tile i being channel i of every such half group
-            const int wd = warp & 7, kh = warp >> 3, g = lane >> 2, t4 = lane & 3;
+            // ---- P V: warp owns channels 128 (w % 4) .. + 127 of keys 64 (w / 4) .. + 63; lane (g, t)
+            // converts channels 16 g .. + 15 of those (one scale group) of the keys of its B
+            // fragments, n-tile i being channel i of every group
+            const int wq = warp & 3, kh = warp >> 2, g = lane >> 2, t4 = lane & 3;
             // byte offsets in a stage of the lane's codes of keys 2 t and 2 t + 1 (their swizzles),
             // and of their scales; in P of the row that the lane hands to ldmatrix
-            const uint32_t code0 = (wd >> 2) * (AC_CODE_BYTES / 2) + (64 * kh + 2 * t4) * 128 + (g & 3) * 4 +
-                                   ((((wd & 3) * 2 + (g >> 2)) ^ (2 * t4)) << 4);
-            const uint32_t code1 = (wd >> 2) * (AC_CODE_BYTES / 2) + (64 * kh + 2 * t4 + 1) * 128 + (g & 3) * 4 +
-                                   ((((wd & 3) * 2 + (g >> 2)) ^ (2 * t4 + 1)) << 4);
-            const uint32_t scale0 = AC_CODE_BYTES + (64 * kh + 2 * t4) * ROW_SCALES + wd * 4 + (g >> 1);
+            const uint32_t panel = (wq >> 1) * (AC_CODE_BYTES / 2) + (64 * kh + 2 * t4) * 128 + (g & 1) * 8;
+            const uint32_t chunk = (wq & 1) * 4 + (g >> 1);
+            const uint32_t code0 = panel + ((chunk ^ (2 * t4)) << 4), code1 = panel + 128 + ((chunk ^ (2 * t4 + 1)) << 4);
+            const uint32_t scale0 = AC_CODE_BYTES + (64 * kh + 2 * t4) * ROW_SCALES + wq * 8 + g;
             const uint32_t stage0 = smem_u32(sm.stage[0]);
             const uint32_t p0 = smem_u32(sm.p[0]) + (64 * kh + ((lane >> 4) << 3) + (lane & 7)) * 32 +
                                 ((((lane >> 3) ^ (lane >> 2)) & 1) << 4);
@@ -720,27 +721,27 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                 if (rw > 0) row = next_row(p, row);
                 const int tiles = row_view(p, row).tiles;
                 const int end = min(tiles, tile + left);
-                float o[8][4] = {};
+                float o[16][4] = {};
                 float m0 = -INFINITY, m1 = -INFINITY;        // references of heads g, g + 8 that o stands at
-                uint32_t ready = 0;                          // P of the next tile seen already
                 for (int t = tile; t < end; ++t, ++it) {
                     const int st = it % AC_STAGES, buf = it & 1;
-                    if (!ready) wait(&sm.p_full[buf], it >> 1);
-                    const uint32_t sa = stage0 + st * AC_STAGE_BYTES, ca0 = sa + code0, ca1 = sa + code1, xa = sa + scale0;
-                    const uint32_t pa = p0 + buf * AC_P_BYTES;
+                    const uint32_t sa = stage0 + st * AC_STAGE_BYTES, pa = p0 + buf * AC_P_BYTES;
+                    wait(&sm.full[st], it / AC_STAGES);
+                    wait(&sm.p_full[buf], it >> 1);
                     // step ks + 1's operands are loaded while step ks is multiplied
-                    uint32_t a[2][4], c[2][4], sc[2][4];
+                    uint32_t a[2][4], sc[2][4];
+                    uint2 c[2][4];
                     auto load_step = [&](int ks) {           // keys 16 ks + 2 t + {0, 1, 8, 9}
                         const int n = ks & 1;
-                        ldmatrix_x4_trans(a[n], pa + ks * 16 * 32);
-                        c[n][0] = lds32(ca0 + ks * 2048);
-                        c[n][1] = lds32(ca1 + ks * 2048);
-                        c[n][2] = lds32(ca0 + ks * 2048 + 1024);
-                        c[n][3] = lds32(ca1 + ks * 2048 + 1024);
-                        sc[n][0] = lds8(xa + ks * 512);
-                        sc[n][1] = lds8(xa + ks * 512 + 32);
-                        sc[n][2] = lds8(xa + ks * 512 + 256);
-                        sc[n][3] = lds8(xa + ks * 512 + 288);
+                        ldmatrix_x4_trans(a[n], pa + ks * 512);
+                        c[n][0] = lds64(sa + code0 + ks * 2048);
+                        c[n][1] = lds64(sa + code1 + ks * 2048);
+                        c[n][2] = lds64(sa + code0 + ks * 2048 + 1024);
+                        c[n][3] = lds64(sa + code1 + ks * 2048 + 1024);
+                        sc[n][0] = lds8(sa + scale0 + ks * 512);
+                        sc[n][1] = lds8(sa + scale0 + ks * 512 + 32);
+                        sc[n][2] = lds8(sa + scale0 + ks * 512 + 256);
+                        sc[n][3] = lds8(sa + scale0 + ks * 512 + 288);
                     };
                     load_step(0);
                     if (sm.moved[buf]) {
@@ -749,7 +750,7 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         m0 = n0;
                         m1 = n1;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < 16; ++i) {
                             o[i][0] *= a0;
                             o[i][1] *= a0;
                             o[i][2] *= a1;
@@ -760,19 +761,23 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                     for (int ks = 0; ks < 4; ++ks) {
                         const int n = ks & 1;
                         if (ks < 3) load_step(ks + 1);
-                        else ready = t + 1 < end ? poll(&sm.p_full[buf ^ 1], (it + 1) >> 1) : 0u;
                         const uint32_t s0 = scales_to_f16x2(__byte_perm(sc[n][0], sc[n][1], 0x40));
                         const uint32_t s1 = scales_to_f16x2(__byte_perm(sc[n][2], sc[n][3], 0x40));
-                        // two keys' codes interleaved: byte i of ev / od = channel 2 i / 2 i + 1 of both
-                        uint32_t e0[4], e1[4], d0[4], d1[4];
-                        e2m1x8_to_f16((c[n][0] & 0x0F0F0F0Fu) | ((c[n][1] << 4) & 0xF0F0F0F0u), e0);
-                        e2m1x8_to_f16((c[n][2] & 0x0F0F0F0Fu) | ((c[n][3] << 4) & 0xF0F0F0F0u), e1);
-                        e2m1x8_to_f16(((c[n][0] >> 4) & 0x0F0F0F0Fu) | (c[n][1] & 0xF0F0F0F0u), d0);
-                        e2m1x8_to_f16(((c[n][2] >> 4) & 0x0F0F0F0Fu) | (c[n][3] & 0xF0F0F0F0u), d1);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            mma_16816(o[2 * i], a[n], mul_f16x2(e0[i], s0), mul_f16x2(e1[i], s1));
-                            mma_16816(o[2 * i + 1], a[n], mul_f16x2(d0[i], s0), mul_f16x2(d1[i], s1));
+                        for (int hw = 0; hw < 2; ++hw) {     // channels 8 hw .. + 7
+                            const uint32_t a0 = hw ? c[n][0].y : c[n][0].x, a1 = hw ? c[n][1].y : c[n][1].x;
+                            const uint32_t b0 = hw ? c[n][2].y : c[n][2].x, b1 = hw ? c[n][3].y : c[n][3].x;
+                            // two keys' codes interleaved: byte i of e / d = channel 2 i / 2 i + 1 of both
+                            uint32_t e0[4], e1[4], d0[4], d1[4];
+                            e2m1x8_to_f16((a0 & 0x0F0F0F0Fu) | ((a1 << 4) & 0xF0F0F0F0u), e0);
+                            e2m1x8_to_f16((b0 & 0x0F0F0F0Fu) | ((b1 << 4) & 0xF0F0F0F0u), e1);
+                            e2m1x8_to_f16(((a0 >> 4) & 0x0F0F0F0Fu) | (a1 & 0xF0F0F0F0u), d0);
+                            e2m1x8_to_f16(((b0 >> 4) & 0x0F0F0F0Fu) | (b1 & 0xF0F0F0F0u), d1);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                mma_16816(o[8 * hw + 2 * i], a[n], mul_f16x2(e0[i], s0), mul_f16x2(e1[i], s1));
+                                mma_16816(o[8 * hw + 2 * i + 1], a[n], mul_f16x2(d0[i], s0), mul_f16x2(d1[i], s1));
+                            }
                         }
                     }
                     __syncwarp();
@@ -781,7 +786,7 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         mbar_arrive(&sm.empty[st]);
                     }
                 }
-                // ---- the key halves: warps 8-15 hand n-tiles 0 .. 3 over and take 4 .. 7
+                // ---- the key halves: warps 4-7 hand n-tiles 0 .. 7 over and take 8 .. 15
                 const bool whole = tile == 0 && end == tiles;
                 const int slot = 2 * blockIdx.x + (tile == 0 ? 1 : 0);     // 0: the row this range starts in
                 float* part = p.part + static_cast<int64_t>(slot) * CACHE_PART_FLOATS;
@@ -789,24 +794,24 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                 wait(&sm.r_full[rb], rw >> 1);
                 if (kh) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sm.x[wd][i][lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                    for (int i = 0; i < 8; ++i) sm.x[wq][i][lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
                 }
-                named_barrier(BAR_PV + wd, 64);
+                named_barrier(BAR_PV + wq, 64);
                 if (!kh) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 u = sm.x[wd][i][lane];
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 u = sm.x[wq][i][lane];
                         o[i][0] += u.x, o[i][1] += u.y, o[i][2] += u.z, o[i][3] += u.w;
-                        sm.x[wd][i][lane] = make_float4(o[4 + i][0], o[4 + i][1], o[4 + i][2], o[4 + i][3]);
+                        sm.x[wq][i][lane] = make_float4(o[8 + i][0], o[8 + i][1], o[8 + i][2], o[8 + i][3]);
                     }
                 }
-                named_barrier(BAR_PV + wd, 64);
+                named_barrier(BAR_PV + wq, 64);
                 if (kh) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 u = sm.x[wd][i][lane];
-                        o[i][0] = o[4 + i][0] + u.x, o[i][1] = o[4 + i][1] + u.y;
-                        o[i][2] = o[4 + i][2] + u.z, o[i][3] = o[4 + i][3] + u.w;
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 u = sm.x[wq][i][lane];
+                        o[i][0] = o[8 + i][0] + u.x, o[i][1] = o[8 + i][1] + u.y;
+                        o[i][2] = o[8 + i][2] + u.z, o[i][3] = o[8 + i][3] + u.w;
                     }
                 }
 #pragma unroll
@@ -815,17 +820,25 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                     const float ls = sm.l[rb][0][h] + sm.l[rb][1][h] + sm.l[rb][2][h] + sm.l[rb][3][h];
                     const float inv = whole ? 1.0f / ls : 1.0f;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {            // channels 8 (2 t + e) + 4 kh .. + 3 of the warp's
-                        const int ch = 64 * wd + 8 * (2 * t4 + e) + 4 * kh;
-                        const float4 val = make_float4(o[0][2 * hh + e] * inv, o[1][2 * hh + e] * inv, o[2][2 * hh + e] * inv,
-                                                       o[3][2 * hh + e] * inv);
+                    for (int e = 0; e < 2; ++e) {            // channels 16 (2 t + e) + 8 kh .. + 7 of the warp's
+                        const int ch = 128 * wq + 16 * (2 * t4 + e) + 8 * kh;
+                        float val[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) val[i] = o[i][2 * hh + e] * inv;
                         const int64_t at = (static_cast<int64_t>(row) * HEADS + h) * D + ch;
                         if (whole && !p.out_f32) {
-                            const __nv_bfloat162 a = __floats2bfloat162_rn(val.x, val.y), b = __floats2bfloat162_rn(val.z, val.w);
-                            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
-                                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const __nv_bfloat162 two = __floats2bfloat162_rn(val[2 * i], val[2 * i + 1]);
+                                w[i] = *reinterpret_cast<const uint32_t*>(&two);
+                            }
+                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
                         } else {
-                            *reinterpret_cast<float4*>(whole ? static_cast<float*>(p.out) + at : part + 2 * HEADS + h * D + ch) = val;
+                            float4* dst = reinterpret_cast<float4*>(whole ? static_cast<float*>(p.out) + at
+                                                                          : part + 2 * HEADS + h * D + ch);
+                            dst[0] = make_float4(val[0], val[1], val[2], val[3]);
+                            dst[1] = make_float4(val[4], val[5], val[6], val[7]);
                         }
                     }
                     if (warp == 0 && t4 == 0) {
