@@ -420,23 +420,29 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
     }
     griddep_launch_dependents();
     griddep_wait();                                         // nothing global is touched before
-    // Every wait is bounded: by `limit` polls, each of which may suspend the thread for about
-    // `nap` ns.  One that runs out flags ERR_TIMEOUT and sets limit to 0: from then on this
-    // thread polls once per wait, issues no copy and no MMA, and takes part in every barrier
-    // and arrival as before, so that all warps reach the end.
+    // Every wait is bounded: by `limit` polls (after a first one that never blocks, the default
+    // bound's may suspend the thread for a while).  One that runs out flags ERR_TIMEOUT and sets
+    // limit to 0: from then on this thread polls once per wait, issues no copy and no MMA, and
+    // takes part in every barrier and arrival as before, so that all warps reach the end.
     unsigned* err = p.err;
     uint32_t limit = wait_limit(err);
-    const uint32_t nap = limit == SPIN_LIMIT ? 1000u : 0u;
-    auto poll = [&](uint64_t* bar, int phase) {
+    const bool block = limit == SPIN_LIMIT;
+    auto done = [&](uint64_t* bar, int phase) {             // one look
         uint32_t ok;
-        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
-                     : "=r"(ok) : "r"(smem_u32(bar)), "r"(static_cast<uint32_t>(phase & 1)), "r"(nap) : "memory");
+        asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(ok) : "r"(smem_u32(bar)), "r"(static_cast<uint32_t>(phase & 1)) : "memory");
         return ok;
     };
     auto wait = [&](uint64_t* bar, int phase) {
-        uint32_t n = 0, ok;
-        do ok = poll(bar, phase);
-        while (!ok && ++n < limit);
+        const uint32_t addr = smem_u32(bar), parity = static_cast<uint32_t>(phase & 1);
+        uint32_t n = 0, ok = done(bar, phase);
+        while (!ok && ++n < limit) {
+            if (block)
+                asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                             : "=r"(ok) : "r"(addr), "r"(parity) : "memory");
+            else
+                ok = done(bar, phase);
+        }
         if (!ok) {
             limit = 0;
             atomicOr(err, ERR_TIMEOUT);
@@ -519,22 +525,29 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
             const uint64_t dq = umma_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
             const uint64_t dc = umma_desc_sw128(smem_u32(sm.stage[0]), 16, 1024);
             const uint64_t ds = desc_rows16(smem_u32(sm.sf[0][0]));
+            // this warp's half of the next row's query is prepared a head per tile while the current
+            // row runs, what is left of it at the row's end
+            const int head0 = buf * (HEADS / 2);
+            int next = row;
+            if (left > 0 && lane == 0) mbar_arrive(&sm.q_full[0]);       // the first row's is there
             while (left > 0) {
                 const int qb = rw & 1;
-                if (rw > 0) {
-                    row = next_row(p, row);
-                    if (rw >= 2) wait(&sm.q_empty[qb], (rw >> 1) - 1);
-#pragma unroll 1
-                    for (int h = buf * (HEADS / 2); h < (buf + 1) * (HEADS / 2); h += 2) {
-                        const QueryHead a = load_query(p, row, h), b = load_query(p, row, h + 1);
-                        put_query(p, sm, qb, h, a);
-                        put_query(p, sm, qb, h + 1, b);
-                    }
-                    fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.q_full[qb]);
+                row = next;
                 const int end = min(row_view(p, row).tiles, tile + left);
+                int heads = left > end - tile ? 0 : HEADS / 2;               // of the next row, done
+                if (heads == 0) {
+                    next = next_row(p, row + 1);
+                    if (rw >= 1) wait(&sm.q_empty[qb ^ 1], ((rw + 1) >> 1) - 1);
+                }
+                auto prepare_head = [&]() {
+                    const int h = head0 + heads++;
+                    put_query(p, sm, qb ^ 1, h, load_query(p, next, h));
+                    if (heads == HEADS / 2) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.q_full[qb ^ 1]);
+                    }
+                };
                 wait(&sm.q_full[qb], rw >> 1);
                 const uint64_t dqr = dq + qb * (2 * AC_QPANEL / 16);
                 for (int t = tile; t < end; ++t, ++it) {
@@ -571,10 +584,11 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         mma_commit(&sm.s_full[buf]);
                     }
                     __syncwarp();
+                    if (heads < HEADS / 2) prepare_head();
                 }
+                while (heads < HEADS / 2) prepare_head();
                 left -= end - tile;
                 tile = 0;
-                ++row;
                 ++rw;
             }
             if (lane == 0) {
@@ -682,6 +696,7 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         z[0] = z[1] = make_uint4(0u, 0u, 0u, 0u);
                         fence_proxy_async_smem();            // before the next copy into this stage
                     }
+                    wait(&sm.full[st], it / AC_STAGES);      // P V reads the tile on this word
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.p_full[buf]);
                 }
@@ -723,11 +738,11 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                 const int end = min(tiles, tile + left);
                 float o[16][4] = {};
                 float m0 = -INFINITY, m1 = -INFINITY;        // references of heads g, g + 8 that o stands at
+                uint32_t ready = 0;                          // P of the next tile seen already
                 for (int t = tile; t < end; ++t, ++it) {
                     const int st = it % AC_STAGES, buf = it & 1;
                     const uint32_t sa = stage0 + st * AC_STAGE_BYTES, pa = p0 + buf * AC_P_BYTES;
-                    wait(&sm.full[st], it / AC_STAGES);
-                    wait(&sm.p_full[buf], it >> 1);
+                    if (!ready) wait(&sm.p_full[buf], it >> 1);
                     // step ks + 1's operands are loaded while step ks is multiplied
                     uint32_t a[2][4], sc[2][4];
                     uint2 c[2][4];
@@ -761,6 +776,7 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                     for (int ks = 0; ks < 4; ++ks) {
                         const int n = ks & 1;
                         if (ks < 3) load_step(ks + 1);
+                        else ready = t + 1 < end ? done(&sm.p_full[buf ^ 1], (it + 1) >> 1) : 0u;
                         const uint32_t s0 = scales_to_f16x2(__byte_perm(sc[n][0], sc[n][1], 0x40));
                         const uint32_t s1 = scales_to_f16x2(__byte_perm(sc[n][2], sc[n][3], 0x40));
 #pragma unroll
@@ -873,74 +889,83 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
 // and are added up in group order.
 constexpr int AJ_SLICES = 16;
 constexpr int AJ_GROUPS = 4;
+constexpr int AJ_AHEAD = 2;
 constexpr int AJ_THREADS = 128 * AJ_GROUPS;
+static_assert(AJ_THREADS >= CACHE_MAX_RANGES, "a thread per range");
 
 __global__ void __launch_bounds__(AJ_THREADS)
 join_cache_kernel(CacheParams p) {
-    __shared__ int32_t meta[2 * CACHE_MAX_RANGES];
     __shared__ float w[CACHE_MAX_RANGES][HEADS], lw[CACHE_MAX_RANGES][HEADS];
-    __shared__ int sh_first, sh_last;
+    __shared__ int ends[AJ_THREADS / 32], sh_first, sh_last, sh_row;
     __shared__ float4 acc[AJ_GROUPS - 1][128];
     const int tid = threadIdx.x, lane = tid & 31;
     griddep_wait();
-    for (int i = tid; i < 2 * p.ranges; i += AJ_THREADS) meta[i] = __ldcg(p.meta + i);
-    if (tid == 0) sh_last = -1;
+    // thread g: range g's partials' rows, and whether its first one ends a row
+    int r0 = -1, r1 = -1;
+    bool end = false;
+    if (tid < p.ranges) {
+        const int2 m = __ldcg(reinterpret_cast<const int2*>(p.meta) + tid);
+        const int after = tid + 1 < p.ranges ? __ldcg(p.meta + 2 * tid + 2) : -1;
+        r0 = m.x, r1 = m.y;
+        end = r0 >= 0 && after != r0;
+    }
+    const unsigned mine = __ballot_sync(0xFFFFFFFFu, end);
+    if (lane == 0) ends[tid / 32] = __popc(mine);
+    if (tid == 0) sh_row = -1;
     __syncthreads();
-    if (tid < 32) {
-        int seen = 0, last = -1, first = -1;
-        for (int g0 = 0; g0 < p.ranges && last < 0; g0 += 32) {
-            const int g = g0 + lane;
-            const bool end = g < p.ranges && meta[2 * g] >= 0 && (g + 1 >= p.ranges || meta[2 * g + 2] != meta[2 * g]);
-            unsigned any = __ballot_sync(0xFFFFFFFFu, end);
-            for (; any && last < 0; any &= any - 1)
-                if (seen++ == static_cast<int>(blockIdx.x)) last = g0 + __ffs(any) - 1;
-        }
-        if (last >= 0) {                                    // the range whose second partial is this row's
-            for (int g0 = last; first < 0; g0 -= 32) {
-                const int g = g0 - lane;
-                const unsigned any = __ballot_sync(0xFFFFFFFFu, g <= 0 || meta[2 * g + 1] == meta[2 * last]);
-                if (any) first = max(0, g0 - (__ffs(any) - 1));
-            }
-        }
-        if (lane == 0) {
-            sh_first = first;
-            sh_last = last;
-        }
+    int before = __popc(mine & ((1u << lane) - 1u));
+    for (int i = 0; i < tid / 32; ++i) before += ends[i];
+    if (end && before == static_cast<int>(blockIdx.x)) {
+        sh_last = tid;
+        sh_row = r0;
     }
     __syncthreads();
-    const int first = sh_first, last = sh_last, n = last - first + 1;
-    if (last < 0) return;
+    const int row = sh_row;
+    if (row < 0) return;
+    if (r1 == row) sh_first = tid;
+    __syncthreads();
+    const int first = sh_first, n = sh_last - first + 1;
     auto part = [&](int i) { return p.part + static_cast<int64_t>(2 * (first + i) + (i == 0 ? 1 : 0)) * CACHE_PART_FLOATS; };
+    const int grp = tid / 128, h = (tid % 128) / 8, c = blockIdx.y * (D / AJ_SLICES) + (tid % 8) * 4;
+    float4 v[AJ_AHEAD];                                     // the group's first ones, on their way with the statistics
+#pragma unroll
+    for (int k = 0; k < AJ_AHEAD; ++k) {
+        const int i = grp + k * AJ_GROUPS;
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n) v[k] = __ldcg(reinterpret_cast<const float4*>(part(i) + 2 * HEADS + h * D + c));
+    }
     for (int i = tid; i < n * HEADS; i += AJ_THREADS) {
         w[i / HEADS][i % HEADS] = __ldcg(part(i / HEADS) + i % HEADS);
         lw[i / HEADS][i % HEADS] = __ldcg(part(i / HEADS) + HEADS + i % HEADS);
     }
     __syncthreads();
-    const int64_t row = meta[2 * last];
-    const int grp = tid / 128, h = (tid % 128) / 8, c = blockIdx.y * (D / AJ_SLICES) + (tid % 8) * 4;
     float m = -INFINITY, l = 0.0f;
     for (int i = 0; i < n; ++i) m = fmaxf(m, w[i][h]);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = grp; i < n; i += AJ_GROUPS) {
+    auto take = [&](int i, const float4& u) {
         const float a = fast_exp2(w[i][h] - m);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(part(i) + 2 * HEADS + h * D + c));
-        o.x = fmaf(a, v.x, o.x);
-        o.y = fmaf(a, v.y, o.y);
-        o.z = fmaf(a, v.z, o.z);
-        o.w = fmaf(a, v.w, o.w);
-    }
+        o.x = fmaf(a, u.x, o.x);
+        o.y = fmaf(a, u.y, o.y);
+        o.z = fmaf(a, u.z, o.z);
+        o.w = fmaf(a, u.w, o.w);
+    };
+#pragma unroll
+    for (int k = 0; k < AJ_AHEAD; ++k)
+        if (grp + k * AJ_GROUPS < n) take(grp + k * AJ_GROUPS, v[k]);
+#pragma unroll 4
+    for (int i = grp + AJ_AHEAD * AJ_GROUPS; i < n; i += AJ_GROUPS)
+        take(i, __ldcg(reinterpret_cast<const float4*>(part(i) + 2 * HEADS + h * D + c)));
     if (grp) acc[grp - 1][tid % 128] = o;
     __syncthreads();
     if (grp) return;
     for (int i = 0; i < n; ++i) l = fmaf(fast_exp2(w[i][h] - m), lw[i][h], l);
 #pragma unroll
     for (int i = 0; i < AJ_GROUPS - 1; ++i) {
-        const float4 v = acc[i][tid];
-        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+        const float4 u = acc[i][tid];
+        o.x += u.x, o.y += u.y, o.z += u.z, o.w += u.w;
     }
     const float inv = 1.0f / l;
-    const int64_t at = (row * HEADS + h) * D + c;
+    const int64_t at = (static_cast<int64_t>(row) * HEADS + h) * D + c;
     if (p.out_f32) {
         *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     } else {
@@ -948,7 +973,7 @@ join_cache_kernel(CacheParams p) {
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     }
-    if (p.lse && blockIdx.y == 0 && tid % 8 == 0) p.lse[row * HEADS + h] = (m + log2f(l)) * LN2;
+    if (p.lse && blockIdx.y == 0 && tid % 8 == 0) p.lse[static_cast<int64_t>(row) * HEADS + h] = (m + log2f(l)) * LN2;
 }
 
 }  // namespace
