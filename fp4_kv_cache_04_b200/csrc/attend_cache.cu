@@ -127,12 +127,12 @@ __device__ __forceinline__ void empty_rows(const CacheParams& p) {
 }
 
 // ---------------------------------------------------------------- the kernel
-constexpr int AC_THREADS = 480;
+constexpr int AC_THREADS = 512;
 constexpr int AC_PV_WARPS = 8;                     // warps 0-3, 4-7: P V of a tile's first / last 64 keys
 constexpr int AC_SM_WARP = 8;                      // warps 8-11: softmax (TMEM lane quarters 0-3)
 constexpr int AC_TMA_WARP = 12;
-constexpr int AC_MMA_WARP = 13;                    // warps 13, 14: scales and MMAs of even / odd tiles,
-                                                   // and half of the next row's query each
+constexpr int AC_MMA_WARP = 13;                    // warps 13, 14: scales and MMAs of even / odd tiles
+constexpr int AC_Q_WARP = 15;                      // the next row's query, shared with warps 13 and 14
 constexpr int AC_STAGES = 4;
 constexpr int AC_CODE_BYTES = CACHE_TILE * ROW_CODES;                    // two panels of 16 KB
 constexpr int AC_STAGE_BYTES = AC_CODE_BYTES + CACHE_TILE * ROW_SCALES;  // 36 KB
@@ -392,7 +392,7 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
             mbar_init(&sm.s_empty[i], 4);
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.p_empty[i], AC_PV_WARPS);
-            mbar_init(&sm.q_full[i], 2);
+            mbar_init(&sm.q_full[i], 3);
             mbar_init(&sm.q_empty[i], 4);                   // the softmax warps: they saw the row's last S
             mbar_init(&sm.r_full[i], 4);
             mbar_init(&sm.r_empty[i], AC_PV_WARPS);
@@ -455,6 +455,34 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
     int it = 0, rw = 0;
     int row = range.row, left = range.count, tile = range.tile;
 
+    // the first row's query, a head per warp
+    auto first_query = [&]() {
+        if (range.count > 0) {
+            put_query(p, sm, 0, warp, load_query(p, range.row, warp));
+            fence_proxy_async_smem();
+        }
+        __syncthreads();
+        tc_fence_after();
+    };
+    // the following rows' ones: heads [h0, h1) by this warp, the next one's values on their way
+    QueryHead ahead;
+    int heads = 0, h0 = 0, h1 = 0, next = range.row;
+    auto begin_query = [&](int qb) {                        // of row `next` into buffer qb
+        heads = h0;
+        ahead = load_query(p, next, heads);
+        if (rw >= 1) wait(&sm.q_empty[qb], ((rw + 1) >> 1) - 1);
+    };
+    auto prepare_head = [&](int qb) {
+        const QueryHead v = ahead;
+        if (heads + 1 < h1) ahead = load_query(p, next, heads + 1);
+        put_query(p, sm, qb, heads, v);
+        if (++heads == h1) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_full[qb]);
+        }
+    };
+
     if (warp == AC_TMA_WARP) {
         // ---- producer: runs ahead over the rows, AC_STAGES tiles at most
         uint64_t policy;
@@ -477,7 +505,7 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                     // the first row's query is still being written: its barrier comes once the
                     // ring is full or the row is loaded
                     if (first && it == AC_STAGES) {
-                        __syncthreads();
+                        first_query();
                         first = false;
                     }
                     if (lane == 0) {
@@ -495,13 +523,13 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                     __syncwarp();
                 }
             }
-            if (first) __syncthreads();
+            if (first) first_query();
             left -= end - tile;
             tile = 0;
             ++row;
         };
         if (left > 0) load_row(true);
-        else __syncthreads();
+        else first_query();
         while (left > 0) {
             row = next_row(p, row);
             load_row(false);
@@ -511,43 +539,38 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                 if (sm.issued[st]) mbar_wait(&sm.full[st], static_cast<uint32_t>((sm.issued[st] - 1) & 1), err);
         }
     } else {
-        // the first row's query: a head or two per P V and softmax warp; the following rows' by the
-        // MMA warps
-        if (left > 0 && warp < AC_TMA_WARP) {
-#pragma unroll 1
-            for (int h = warp; h < HEADS; h += AC_TMA_WARP) put_query(p, sm, 0, h, load_query(p, row, h));
-            fence_proxy_async_smem();
-        }
-        __syncthreads();
-        tc_fence_after();
+        first_query();
         if (warp >= AC_MMA_WARP) {
+            h0 = (warp - AC_MMA_WARP) * 5;
+            h1 = warp == AC_Q_WARP ? HEADS : h0 + 5;
+            if (left > 0 && lane == 0) mbar_arrive(&sm.q_full[0]);       // the first row's is there
+        }
+        if (warp == AC_Q_WARP) {
+            while (left > 0) {
+                const int end = min(row_view(p, next).tiles, tile + left);
+                if (left > end - tile) {
+                    next = next_row(p, next + 1);
+                    begin_query((rw & 1) ^ 1);
+                    while (heads < h1) prepare_head((rw & 1) ^ 1);
+                }
+                left -= end - tile;
+                tile = 0;
+                ++rw;
+            }
+            empty_rows(p);
+        } else if (warp >= AC_MMA_WARP) {
             const int buf = warp - AC_MMA_WARP;             // tiles of this parity
             const uint64_t dq = umma_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
             const uint64_t dc = umma_desc_sw128(smem_u32(sm.stage[0]), 16, 1024);
             const uint64_t ds = desc_rows16(smem_u32(sm.sf[0][0]));
-            // this warp's half of the next row's query is prepared a head per tile while the current
-            // row runs, what is left of it at the row's end
-            const int head0 = buf * (HEADS / 2);
-            int next = row;
-            if (left > 0 && lane == 0) mbar_arrive(&sm.q_full[0]);       // the first row's is there
             while (left > 0) {
                 const int qb = rw & 1;
                 row = next;
                 const int end = min(row_view(p, row).tiles, tile + left);
-                int heads = left > end - tile ? 0 : HEADS / 2;               // of the next row, done
-                if (heads == 0) {
-                    next = next_row(p, row + 1);
-                    if (rw >= 1) wait(&sm.q_empty[qb ^ 1], ((rw + 1) >> 1) - 1);
-                }
-                auto prepare_head = [&]() {
-                    const int h = head0 + heads++;
-                    put_query(p, sm, qb ^ 1, h, load_query(p, next, h));
-                    if (heads == HEADS / 2) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.q_full[qb ^ 1]);
-                    }
-                };
+                // its share of the next row's query is prepared a head per tile while the current
+                // row runs, what is left of it at the row's end
+                const bool more = left > end - tile;
+                bool begun = false;
                 wait(&sm.q_full[qb], rw >> 1);
                 const uint64_t dqr = dq + qb * (2 * AC_QPANEL / 16);
                 for (int t = tile; t < end; ++t, ++it) {
@@ -584,9 +607,19 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         mma_commit(&sm.s_full[buf]);
                     }
                     __syncwarp();
-                    if (heads < HEADS / 2) prepare_head();
+                    if (more && !begun) {
+                        next = next_row(p, row + 1);
+                        begin_query(qb ^ 1);
+                        begun = true;
+                    } else if (more && heads < h1) {
+                        prepare_head(qb ^ 1);
+                    }
                 }
-                while (heads < HEADS / 2) prepare_head();
+                if (more && !begun) {
+                    next = next_row(p, row + 1);
+                    begin_query(qb ^ 1);
+                }
+                while (more && heads < h1) prepare_head(qb ^ 1);
                 left -= end - tile;
                 tile = 0;
                 ++rw;
@@ -595,7 +628,6 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                 mma_commit(&sm.drain);
                 mbar_wait(&sm.drain, 0, err);
             }
-            if (buf) empty_rows(p);
         } else if (warp >= AC_SM_WARP) {
             // ---- softmax: thread = key
             const int quarter = warp & 3, key = 32 * quarter + lane;
