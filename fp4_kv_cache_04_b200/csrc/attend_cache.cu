@@ -24,13 +24,17 @@ struct RowView {
     __device__ __forceinline__ int pos(int tile) const { return (tile < ts ? tile : w0 + tile - ts) * CACHE_TILE; }
 };
 
-__device__ __forceinline__ RowView row_view(const CacheParams& p, int row) {
+__device__ __forceinline__ int visible_positions(const CacheParams& p, int row) {
     const int b = p.q_per_seq == 1 ? row : row / p.q_per_seq;
     int n = static_cast<int>(max(static_cast<int64_t>(0), min(p.kv_offsets[b + 1] - p.kv_offsets[b], static_cast<int64_t>(p.max_n))));
     if (p.q_pos) {
         const int64_t t = p.q_pos[b] + (row - b * p.q_per_seq) + 1;
         n = static_cast<int>(min(static_cast<int64_t>(n), max(static_cast<int64_t>(0), t) >> (p.ratio - 1)));
     }
+    return n;
+}
+
+__device__ __forceinline__ RowView view_of(const CacheParams& p, int n) {
     RowView v;
     v.n_vis = n;
     v.w_beg = p.window > 0 ? max(0, n - p.window) : 0;
@@ -39,6 +43,8 @@ __device__ __forceinline__ RowView row_view(const CacheParams& p, int row) {
     v.tiles = n > 0 ? v.ts + (n + CACHE_TILE - 1) / CACHE_TILE - v.w0 : 0;
     return v;
 }
+
+__device__ __forceinline__ RowView row_view(const CacheParams& p, int row) { return view_of(p, visible_positions(p, row)); }
 
 __device__ __forceinline__ bool visible(const CacheParams& p, const RowView& v, int j) {
     return j < v.n_vis && (j >= v.w_beg || j < p.sinks);
@@ -134,6 +140,7 @@ constexpr int AC_TMA_WARP = 12;
 constexpr int AC_MMA_WARP = 13;                    // warps 13, 14: scales and MMAs of even / odd tiles
 constexpr int AC_Q_WARP = 15;                      // the next row's query, shared with warps 13 and 14
 constexpr int AC_STAGES = 4;
+constexpr int AC_ROWS = 32;
 constexpr int AC_CODE_BYTES = CACHE_TILE * ROW_CODES;                    // two panels of 16 KB
 constexpr int AC_STAGE_BYTES = AC_CODE_BYTES + CACHE_TILE * ROW_SCALES;  // 36 KB
 constexpr int AC_DIGITS = 6;
@@ -163,6 +170,7 @@ struct alignas(1024) CacheSmem {
     alignas(16) float f[2][HEADS], l[2][4][HEADS], minus_m[2][HEADS];
     alignas(16) float ref[2][HEADS], part_m[4][HEADS];
     int moved[2];
+    int2 rows[AC_ROWS];                            // the range's first rows that see anything: row, positions
     int issued[AC_STAGES];                         // copies issued into each stage
     uint32_t tmem;
     int red[34];
@@ -287,6 +295,33 @@ __device__ __forceinline__ int next_row(const CacheParams& p, int row) {
         if (row > rows - 32) break;
     }
     return rows - 1;
+}
+
+// The k-th row of the range (k counts those that see anything): from the table, or behind the
+// table's end from global memory, `row` being the (k - 1)-th.  Whole warp.
+__device__ __forceinline__ RowView range_row(const CacheParams& p, const CacheSmem& sm, int k, int& row) {
+    if (k < AC_ROWS) {
+        const int2 r = sm.rows[k];
+        row = r.x;
+        return view_of(p, r.y);
+    }
+    row = next_row(p, row + 1);
+    return row_view(p, row);
+}
+
+// Fills the table from row `row` on, as far as `tiles` tiles reach.  One warp.
+__device__ __forceinline__ void list_rows(const CacheParams& p, CacheSmem& sm, int row, int64_t tiles) {
+    const int rows = p.batch * p.q_per_seq, lane = threadIdx.x & 31;
+    int have = 0;
+    for (; row < rows && have < AC_ROWS && tiles > 0; row += 32) {
+        const int n = row + lane < rows && row + lane >= row ? visible_positions(p, row + lane) : 0;
+        const unsigned some = __ballot_sync(0xFFFFFFFFu, n > 0);
+        const int k = have + __popc(some & ((1u << lane) - 1u));
+        if (n > 0 && k < AC_ROWS) sm.rows[k] = make_int2(row + lane, n);
+        have += __popc(some);
+        tiles -= __reduce_add_sync(0xFFFFFFFFu, view_of(p, n).tiles);
+        if (row > rows - 32) break;
+    }
 }
 
 // Head h of a row's query as six balanced base-8 digits: n = rint(q 2^k), 2^15 <= |n| <
@@ -458,37 +493,39 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
     // the first row's query, a head per warp
     auto first_query = [&]() {
         if (range.count > 0) {
-            put_query(p, sm, 0, warp, load_query(p, range.row, warp));
+            const QueryHead v = load_query(p, range.row, warp);
+            if (warp == AC_Q_WARP) list_rows(p, sm, range.row, static_cast<int64_t>(range.tile) + range.count);
+            put_query(p, sm, 0, warp, v);
             fence_proxy_async_smem();
         }
         __syncthreads();
         tc_fence_after();
     };
     // the following rows' ones: heads [h0, h1) by this warp, the next one's values on their way
-    QueryHead ahead;
-    int heads = 0, h0 = 0, h1 = 0, next = range.row;
-    auto begin_query = [&](int qb) {                        // of row `next` into buffer qb
-        heads = h0;
-        ahead = load_query(p, next, heads);
+    int h0 = 0, h1 = 0, next = range.row;
+    bool asked = false;
+    auto next_query = [&](int qb) {                         // of row rw + 1, into buffer qb
+        if (asked) return;
+        asked = true;
+        range_row(p, sm, rw + 1, next);
+        QueryHead ahead = load_query(p, next, h0);
         if (rw >= 1) wait(&sm.q_empty[qb], ((rw + 1) >> 1) - 1);
-    };
-    auto prepare_head = [&](int qb) {
-        const QueryHead v = ahead;
-        if (heads + 1 < h1) ahead = load_query(p, next, heads + 1);
-        put_query(p, sm, qb, heads, v);
-        if (++heads == h1) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.q_full[qb]);
+#pragma unroll 1
+        for (int h = h0; h < h1; ++h) {
+            const QueryHead v = ahead;
+            if (h + 1 < h1) ahead = load_query(p, next, h + 1);
+            put_query(p, sm, qb, h, v);
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_full[qb]);
     };
 
     if (warp == AC_TMA_WARP) {
         // ---- producer: runs ahead over the rows, AC_STAGES tiles at most
         uint64_t policy;
         asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
-        auto load_row = [&](bool first) {
-            const RowView v = row_view(p, row);
+        auto load_row = [&](const RowView& v, bool first) {
             const int end = min(v.tiles, tile + left);
             const int b = row / p.q_per_seq;
             const int64_t off = p.kv_offsets[b];
@@ -510,7 +547,10 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                     }
                     if (lane == 0) {
                         const int st = it % AC_STAGES;
-                        if (it >= AC_STAGES) wait(&sm.empty[st], it / AC_STAGES - 1);
+                        if (it >= AC_STAGES) {
+                            wait(&sm.empty[st], it / AC_STAGES - 1);
+                            wait(&sm.full[st], it / AC_STAGES - 1);      // landed, whoever gave up waiting for it
+                        }
                         if (limit) {
                             uint8_t* dst = sm.stage[st];
                             mbar_arrive_expect_tx(&sm.full[st], AC_STAGE_BYTES);
@@ -526,14 +566,11 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
             if (first) first_query();
             left -= end - tile;
             tile = 0;
-            ++row;
+            ++rw;
         };
-        if (left > 0) load_row(true);
+        if (left > 0) load_row(row_view(p, row), true);
         else first_query();
-        while (left > 0) {
-            row = next_row(p, row);
-            load_row(false);
-        }
+        while (left > 0) load_row(range_row(p, sm, rw, row), false);
         if (lane == 0) {                                    // no copy may land after the CTA is gone
             for (int st = 0; st < AC_STAGES; ++st)
                 if (sm.issued[st]) mbar_wait(&sm.full[st], static_cast<uint32_t>((sm.issued[st] - 1) & 1), err);
@@ -547,12 +584,9 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
         }
         if (warp == AC_Q_WARP) {
             while (left > 0) {
-                const int end = min(row_view(p, next).tiles, tile + left);
-                if (left > end - tile) {
-                    next = next_row(p, next + 1);
-                    begin_query((rw & 1) ^ 1);
-                    while (heads < h1) prepare_head((rw & 1) ^ 1);
-                }
+                const int end = min(range_row(p, sm, rw, row).tiles, tile + left);
+                if (left > end - tile) next_query((rw & 1) ^ 1);
+                asked = false;
                 left -= end - tile;
                 tile = 0;
                 ++rw;
@@ -565,13 +599,11 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
             const uint64_t ds = desc_rows16(smem_u32(sm.sf[0][0]));
             while (left > 0) {
                 const int qb = rw & 1;
-                row = next;
-                const int end = min(row_view(p, row).tiles, tile + left);
-                // its share of the next row's query is prepared a head per tile while the current
-                // row runs, what is left of it at the row's end
-                const bool more = left > end - tile;
-                bool begun = false;
                 wait(&sm.q_full[qb], rw >> 1);
+                const int end = min(range_row(p, sm, rw, row).tiles, tile + left);
+                // its share of the next row's query is prepared once its first tile of this row is
+                // on its way, two tiles ahead of P V
+                const bool more = left > end - tile;
                 const uint64_t dqr = dq + qb * (2 * AC_QPANEL / 16);
                 for (int t = tile; t < end; ++t, ++it) {
                     if ((it & 1) != buf) continue;
@@ -607,19 +639,10 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         mma_commit(&sm.s_full[buf]);
                     }
                     __syncwarp();
-                    if (more && !begun) {
-                        next = next_row(p, row + 1);
-                        begin_query(qb ^ 1);
-                        begun = true;
-                    } else if (more && heads < h1) {
-                        prepare_head(qb ^ 1);
-                    }
+                    if (more) next_query(qb ^ 1);
                 }
-                if (more && !begun) {
-                    next = next_row(p, row + 1);
-                    begin_query(qb ^ 1);
-                }
-                while (more && heads < h1) prepare_head(qb ^ 1);
+                if (more) next_query(qb ^ 1);
+                asked = false;
                 left -= end - tile;
                 tile = 0;
                 ++rw;
@@ -632,14 +655,13 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
             // ---- softmax: thread = key
             const int quarter = warp & 3, key = 32 * quarter + lane;
             while (left > 0) {
-                if (rw > 0) row = next_row(p, row);
-                const RowView v = row_view(p, row);
-                const int end = min(v.tiles, tile + left);
                 const int rb = rw & 1;
+                wait(&sm.q_full[rb], rw >> 1);
+                const RowView v = range_row(p, sm, rw, row);
+                const int end = min(v.tiles, tile + left);
                 uint64_t l2[HEADS / 2];
 #pragma unroll
                 for (int i = 0; i < HEADS / 2; ++i) l2[i] = 0;
-                wait(&sm.q_full[rb], rw >> 1);               // f
                 if (rw >= 2) wait(&sm.r_empty[rb], (rw >> 1) - 1);
                 if (warp == AC_SM_WARP && lane < HEADS) sm.minus_m[rb][lane] = 0.0f;     // the first tile sets it
                 named_barrier(BAR_MAX, 128);
@@ -747,7 +769,6 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                 }
                 left -= end - tile;
                 tile = 0;
-                ++row;
                 ++rw;
             }
         } else {
@@ -765,8 +786,7 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
             const uint32_t p0 = smem_u32(sm.p[0]) + (64 * kh + ((lane >> 4) << 3) + (lane & 7)) * 32 +
                                 ((((lane >> 3) ^ (lane >> 2)) & 1) << 4);
             while (left > 0) {
-                if (rw > 0) row = next_row(p, row);
-                const int tiles = row_view(p, row).tiles;
+                const int tiles = range_row(p, sm, rw, row).tiles;
                 const int end = min(tiles, tile + left);
                 float o[16][4] = {};
                 float m0 = -INFINITY, m1 = -INFINITY;        // references of heads g, g + 8 that o stands at
@@ -903,7 +923,6 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                 if (!whole && tid == 0) p.meta[slot] = row;
                 left -= end - tile;
                 tile = 0;
-                ++row;
                 ++rw;
             }
         }

@@ -301,7 +301,7 @@ def seen_positions(n, t, ratio, window, sinks):
 
 
 def check_attend(csa2, lens, window=0, sinks=0, q_per_seq=1, q_pos=None, ratio=1, page=0, out_type=BF, seed=0, sm_scale=None,
-                 q_gain=2.0, spread=1.0, max_n=None, spoil=False, want_lse=True, stream=None, cache=None, graph=False):
+                 q_gain=2.0, spread=1.0, max_n=None, spoil=False, want_lse=True, stream=None, cache=None, graph=False, every=1):
     B = len(lens)
     lens_t = torch.tensor(lens)
     offs = torch.cat([torch.zeros(1, dtype=torch.int64), lens_t.cumsum(0)]).to(DEV)
@@ -345,7 +345,7 @@ def check_attend(csa2, lens, window=0, sinks=0, q_per_seq=1, q_pos=None, ratio=1
     assert csa2.check_device_status(ws) == 0
     assert (out[R] == 3.0).all()
     worst = 0.0
-    for r in range(R):
+    for r in range(0, R, every):
         b, i = divmod(r, q_per_seq)
         p = seen_positions(lens[b], None if q_pos is None else q_pos[b] + i, ratio, window, sinks)
         if not p.numel():
@@ -405,6 +405,36 @@ def test_attend_cache_many_rows(csa2):
 
 def test_attend_cache_many_empty_rows_and_one_long(csa2):
     check_attend(csa2, [0] * 700 + [5000] + [0] * 300 + [1], seed=10)
+
+
+@pytest.mark.parametrize("long", [0, 1000])
+def test_attend_cache_more_rows_in_a_range_than_its_table_holds(csa2, long):
+    """12,000 rows of 0 to 4 positions: over 60 that see anything for each of 148 ranges, uncut, and
+    (with one longer row among them) cut."""
+    lens = [i % 5 for i in range(12000)]
+    if long:
+        lens[7001] = long
+    check_attend(csa2, lens, seed=11, every=7)
+
+
+def test_attend_cache_gives_up_in_order_and_recovers(csa2):
+    """With a bound of one poll the kernel's waits run out: the call ends with the timeout flag, and
+    the same workspace serves the next call."""
+    codes, scales = make_cache(6000, 31)
+    offs = torch.tensor([0, 5000, 5003, 5003, 6000], device=DEV)
+    q = torch.randn(4, 16, 512, generator=gen(32), device=DEV).to(BF)
+    outs = [torch.empty(4, 16, 512, device=DEV) for _ in range(2)]
+    kw = dict(batch=4, max_n=5000, kv_offsets=offs, codes=codes, scales=scales, q=q, sm_scale=512 ** -0.5)
+    ws = csa2.alloc_workspace(csa2.cache_workspace_size(csa2.cache_args(out=outs[0], **kw)))
+    csa2.attend_cache(csa2.cache_args(out=outs[0], workspace=ws, **kw))
+    assert csa2.check_device_status(ws) == 0
+    csa2.set_wait_limit(ws, 1)
+    csa2.attend_cache(csa2.cache_args(out=outs[1], workspace=ws, **kw))
+    assert csa2.check_device_status(ws) == 5
+    csa2.set_wait_limit(ws, 0)
+    csa2.attend_cache(csa2.cache_args(out=outs[1], workspace=ws, **kw))
+    assert csa2.check_device_status(ws) == 0
+    assert torch.equal(outs[0], outs[1])
 
 
 @pytest.mark.parametrize("gain,spread", [(0.01, 1.0), (20.0, 1.0), (2.0, 60.0), (1e-30, 1.0), (0.0, 1.0), (2.0, 0.004)])
