@@ -337,6 +337,12 @@ def set_wait_limit(workspace: torch.Tensor, polls: int, stream=None) -> None:
 # ------------------------------------------------------------------ dense use of the cache
 
 
+# torch's own calls behind torch.cuda.current_device() and current_stream().cuda_stream, without
+# the objects those make (absent in a torch built without CUDA, where nothing is launched)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(f"libcsa2: {what}")
@@ -354,10 +360,10 @@ def _same_device(args, *tensors) -> None:
 
 def _launch(fn, args, stream, where: str) -> None:
     """Calls fn(args, stream); the current device must be the one the block's tensors are on."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     if dev != args.device:
         raise ValueError(f"libcsa2: {where}: the tensors are on cuda:{args.device}, the current device is cuda:{dev}")
-    status = fn(args.ref, _stream(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(dev))
+    status = fn(args.ref, _stream(stream) if stream is not None else _raw_stream(dev))
     if status:
         raise Csa2Error(status, where)
 
@@ -462,19 +468,20 @@ def dequantize_kv(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, 
     """Cache rows (src_row int64 [n], or rows 0 .. n-1) -> bf16 out [n][512]."""
     n, d = out.shape
     rows, wide = codes.shape
-    if not (codes.dtype is scales.dtype is torch.uint8 and out.dtype is torch.bfloat16 and d == D and wide == ROW_CODES and
-            scales.shape == (rows, ROW_SCALES) and (src_row is None or src_row.dtype is torch.int64 and src_row.numel() == n)):
-        raise ValueError("libcsa2: codes uint8 [rows][256], scales uint8 [rows][32], out bf16 [n][512], src_row int64 [n]")
-    dev = torch.cuda.current_device()
-    if not codes.get_device() == scales.get_device() == out.get_device() == dev or (
-            src_row is not None and src_row.get_device() != dev):
-        raise ValueError("libcsa2: dequantize_kv: the tensors are not on the current device")
-    if not (codes.is_contiguous() and scales.is_contiguous() and out.is_contiguous() and
-            (src_row is None or src_row.is_contiguous())):
-        raise ValueError("libcsa2 takes contiguous tensors")
-    status = _lib.csa2_dequantize_kv(codes.data_ptr(), scales.data_ptr(), rows, None if src_row is None else src_row.data_ptr(),
-                                     n, out.data_ptr(),
-                                     _stream(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(dev))
+    if (codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or out.dtype is not torch.bfloat16 or d != D or
+            wide != ROW_CODES or scales.shape != (rows, ROW_SCALES)):
+        raise ValueError("libcsa2: codes uint8 [rows][256], scales uint8 [rows][32], out bf16 [n][512]")
+    dev = _current_device()
+    if (codes.get_device() != dev or scales.get_device() != dev or out.get_device() != dev or not codes.is_contiguous() or
+            not scales.is_contiguous() or not out.is_contiguous()):
+        raise ValueError("libcsa2: dequantize_kv takes contiguous tensors on the current device")
+    src = None
+    if src_row is not None:
+        if src_row.dtype is not torch.int64 or src_row.numel() != n or src_row.get_device() != dev or not src_row.is_contiguous():
+            raise ValueError("libcsa2: src_row is contiguous int64 [n] on the current device")
+        src = src_row.data_ptr()
+    status = _lib.csa2_dequantize_kv(codes.data_ptr(), scales.data_ptr(), rows, src, n, out.data_ptr(),
+                                     _stream(stream) if stream is not None else _raw_stream(dev))
     if status:
         raise Csa2Error(status, "csa2_dequantize_kv")
 

@@ -455,12 +455,16 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
     }
     griddep_launch_dependents();
     griddep_wait();                                         // nothing global is touched before
+    unsigned* err = p.err;
+    const uint32_t bound = *reinterpret_cast<const volatile unsigned*>(err + 1);      // csa2_set_wait_limit's, or 0
+    const Range range = my_range<AC_THREADS>(p, sm.red);
+    if (tid < 2) p.meta[2 * blockIdx.x + tid] = -1;
+
     // Every wait is bounded: by `limit` polls (after a first one that never blocks, the default
     // bound's may suspend the thread for a while).  One that runs out flags ERR_TIMEOUT and sets
     // limit to 0: from then on this thread polls once per wait, issues no copy and no MMA, and
     // takes part in every barrier and arrival as before, so that all warps reach the end.
-    unsigned* err = p.err;
-    uint32_t limit = wait_limit(err);
+    uint32_t limit = bound ? bound : SPIN_LIMIT;
     const bool block = limit == SPIN_LIMIT;
     auto done = [&](uint64_t* bar, int phase) {             // one look
         uint32_t ok;
@@ -483,9 +487,6 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
             atomicOr(err, ERR_TIMEOUT);
         }
     };
-    const Range range = my_range<AC_THREADS>(p, sm.red);
-    if (tid < 2) p.meta[2 * blockIdx.x + tid] = -1;
-
     // every role walks the range's rows by itself: it counts tiles, rw rows
     int it = 0, rw = 0;
     int row = range.row, left = range.count, tile = range.tile;
@@ -934,21 +935,21 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
 }
 
 // Joins the partials of one cut row.  Block (x, y): the x-th cut row (the x-th range whose
-// first partial is its row's last one), 512 / AJ_SLICES channels.  A row's partials are
+// first partial is its row's last one), 512 / SLICES channels.  A row's partials are
 // partial 1 of the range it starts in and
-// partials 0 of the following ones, in that order: four groups of threads take every fourth
+// partials 0 of the following ones, in that order: GROUPS groups of threads take every GROUPS-th
 // and are added up in group order.
-constexpr int AJ_SLICES = 16;
-constexpr int AJ_GROUPS = 4;
 constexpr int AJ_AHEAD = 2;
-constexpr int AJ_THREADS = 128 * AJ_GROUPS;
+constexpr int AJ_THREADS = 512;
 static_assert(AJ_THREADS >= CACHE_MAX_RANGES, "a thread per range");
 
+template <int SLICES>
 __global__ void __launch_bounds__(AJ_THREADS)
 join_cache_kernel(CacheParams p) {
+    constexpr int GROUP_THREADS = HEADS * (D / SLICES / 4), GROUPS = AJ_THREADS / GROUP_THREADS;
     __shared__ float w[CACHE_MAX_RANGES][HEADS], lw[CACHE_MAX_RANGES][HEADS];
     __shared__ int ends[AJ_THREADS / 32], sh_first, sh_last, sh_row;
-    __shared__ float4 acc[AJ_GROUPS - 1][128];
+    __shared__ float4 acc[GROUPS - 1][GROUP_THREADS];
     const int tid = threadIdx.x, lane = tid & 31;
     griddep_wait();
     // thread g: range g's partials' rows, and whether its first one ends a row
@@ -977,11 +978,12 @@ join_cache_kernel(CacheParams p) {
     __syncthreads();
     const int first = sh_first, n = sh_last - first + 1;
     auto part = [&](int i) { return p.part + static_cast<int64_t>(2 * (first + i) + (i == 0 ? 1 : 0)) * CACHE_PART_FLOATS; };
-    const int grp = tid / 128, h = (tid % 128) / 8, c = blockIdx.y * (D / AJ_SLICES) + (tid % 8) * 4;
+    const int grp = tid / GROUP_THREADS, at = tid % GROUP_THREADS, h = at / (GROUP_THREADS / HEADS),
+              c = blockIdx.y * (D / SLICES) + at % (GROUP_THREADS / HEADS) * 4;
     float4 v[AJ_AHEAD];                                     // the group's first ones, on their way with the statistics
 #pragma unroll
     for (int k = 0; k < AJ_AHEAD; ++k) {
-        const int i = grp + k * AJ_GROUPS;
+        const int i = grp + k * GROUPS;
         v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i < n) v[k] = __ldcg(reinterpret_cast<const float4*>(part(i) + 2 * HEADS + h * D + c));
     }
@@ -1002,29 +1004,29 @@ join_cache_kernel(CacheParams p) {
     };
 #pragma unroll
     for (int k = 0; k < AJ_AHEAD; ++k)
-        if (grp + k * AJ_GROUPS < n) take(grp + k * AJ_GROUPS, v[k]);
+        if (grp + k * GROUPS < n) take(grp + k * GROUPS, v[k]);
 #pragma unroll 4
-    for (int i = grp + AJ_AHEAD * AJ_GROUPS; i < n; i += AJ_GROUPS)
+    for (int i = grp + AJ_AHEAD * GROUPS; i < n; i += GROUPS)
         take(i, __ldcg(reinterpret_cast<const float4*>(part(i) + 2 * HEADS + h * D + c)));
-    if (grp) acc[grp - 1][tid % 128] = o;
+    if (grp) acc[grp - 1][at] = o;
     __syncthreads();
     if (grp) return;
     for (int i = 0; i < n; ++i) l = fmaf(fast_exp2(w[i][h] - m), lw[i][h], l);
 #pragma unroll
-    for (int i = 0; i < AJ_GROUPS - 1; ++i) {
-        const float4 u = acc[i][tid];
+    for (int i = 0; i < GROUPS - 1; ++i) {
+        const float4 u = acc[i][at];
         o.x += u.x, o.y += u.y, o.z += u.z, o.w += u.w;
     }
     const float inv = 1.0f / l;
-    const int64_t at = (static_cast<int64_t>(row) * HEADS + h) * D + c;
+    const int64_t dst = (static_cast<int64_t>(row) * HEADS + h) * D + c;
     if (p.out_f32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     } else {
         const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + dst) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     }
-    if (p.lse && blockIdx.y == 0 && tid % 8 == 0) p.lse[static_cast<int64_t>(row) * HEADS + h] = (m + log2f(l)) * LN2;
+    if (p.lse && blockIdx.y == 0 && at % (GROUP_THREADS / HEADS) == 0) p.lse[static_cast<int64_t>(row) * HEADS + h] = (m + log2f(l)) * LN2;
 }
 
 }  // namespace
@@ -1052,8 +1054,10 @@ csa2_status launch_attend_cache(const CacheParams& p, const CUtensorMap& codes, 
     csa2_status st = check_launch("attend_cache_kernel");
     if (st != CSA2_OK || p.ranges == 1 || p.whole_rows) return st;
     const int64_t rows = static_cast<int64_t>(p.batch) * p.q_per_seq;
-    launch_dependent(join_cache_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(rows, p.ranges - 1)), AJ_SLICES), AJ_THREADS, 0,
-                     stream, p);
+    // 16 slices of a row while all blocks are resident at once (four to an SM), else 8
+    const unsigned cut = static_cast<unsigned>(std::min<int64_t>(rows, p.ranges - 1));
+    if (cut * 16 <= 4 * CACHE_MAX_RANGES) launch_dependent(join_cache_kernel<16>, dim3(cut, 16), AJ_THREADS, 0, stream, p);
+    else launch_dependent(join_cache_kernel<8>, dim3(cut, 8), AJ_THREADS, 0, stream, p);
     return check_launch("join_cache_kernel");
 }
 
