@@ -94,7 +94,6 @@ struct CacheParams {
 constexpr int CACHE_TILE = 128;                                  // positions per tile
 constexpr int CACHE_MAX_RANGES = 148;                            // one CTA per SM
 constexpr int CACHE_PART_FLOATS = 2 * HEADS + HEADS * D;
-constexpr int CACHE_UNCUT_TILES = 4;
 struct CachePlan {
     int ranges;
     bool whole_rows;
