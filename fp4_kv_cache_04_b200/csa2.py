@@ -354,7 +354,6 @@ def _same_device(args, *tensors) -> None:
     devs = {t.device for t in tensors if t is not None}
     _need(len(devs) == 1, f"tensors on different devices: {sorted(map(str, devs))}")
     args.device = devs.pop().index
-    args.ref = ctypes.byref(args)
     args.tensors = tensors                     # alive as long as the block that points at them
 
 
@@ -363,7 +362,7 @@ def _launch(fn, args, stream, where: str) -> None:
     dev = _current_device()
     if dev != args.device:
         raise ValueError(f"libcsa2: {where}: the tensors are on cuda:{args.device}, the current device is cuda:{dev}")
-    status = fn(args.ref, _stream(stream) if stream is not None else _raw_stream(dev))
+    status = fn(args, _stream(stream) if stream is not None else _raw_stream(dev))
     if status:
         raise Csa2Error(status, where)
 

@@ -85,6 +85,11 @@ struct CacheLayout {
     size_t meta = 0, part = 0, total = 0;
 };
 
+// Positions of a row and rows are counted in 32 bits.
+bool cache_sizes_fit(const csa2_cache_args* a) {
+    return a->max_n <= INT32_MAX && static_cast<int64_t>(a->batch) * a->q_per_seq <= INT32_MAX;
+}
+
 CacheLayout cache_layout(const csa2_cache_args* a) {
     CacheLayout L;
     L.plan = cache_plan(static_cast<int64_t>(a->batch) * a->q_per_seq, a->max_n, a->window, a->sinks);
@@ -595,8 +600,8 @@ csa2_status csa2_norm_rope(const csa2_rope_args* a, void* stream) {
         return CSA2_ERR_INVALID_ARG;
     // two vectors of out must not overlap: heads inside a row, or rows inside a head
     if (a->heads > 1 && a->out_head_stride < a->dim) return CSA2_ERR_INVALID_ARG;
-    const int64_t row_span = (a->heads - 1) * a->out_head_stride + a->dim;
-    const int64_t col_span = (a->rows - 1) * a->out_row_stride + a->dim;
+    const __int128 row_span = static_cast<__int128>(a->heads - 1) * a->out_head_stride + a->dim;
+    const __int128 col_span = static_cast<__int128>(a->rows - 1) * a->out_row_stride + a->dim;
     if (a->rows > 1 && !(a->out_row_stride >= row_span ||
                          (a->out_row_stride >= a->dim && (a->heads == 1 || a->out_head_stride >= col_span))))
         return CSA2_ERR_INVALID_ARG;
@@ -678,7 +683,8 @@ csa2_status csa2_append_rope(const csa2_append_args* a, void* stream) {
 }
 
 size_t csa2_cache_workspace_size(const csa2_cache_args* a) {
-    if (!a || a->batch < 1 || a->q_per_seq < 1 || a->max_n < 1) return 0;
+    if (!a || a->batch < 1 || a->q_per_seq < 1 || a->max_n < 1 || a->window < 0 || a->sinks < 0) return 0;
+    if (!cache_sizes_fit(a)) return 0;
     return cache_layout(a).total;
 }
 
@@ -690,8 +696,8 @@ csa2_status csa2_attend_cache(const csa2_cache_args* a, void* stream) {
         return valid_type(a->out_type) ? CSA2_ERR_UNSUPPORTED : CSA2_ERR_INVALID_ARG;
     if (a->reserved0 != 0 || a->max_n < 1 || a->total_n < 1 || a->total_n > INT32_MAX || a->window < 0 || a->sinks < 0)
         return CSA2_ERR_INVALID_ARG;
-    if (a->max_n > INT32_MAX || static_cast<int64_t>(a->batch) * a->q_per_seq > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
-    if (ceil_div(a->max_n, CACHE_TILE) * a->batch * a->q_per_seq > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
+    if (!cache_sizes_fit(a)) return CSA2_ERR_UNSUPPORTED;
+    if (ceil_div(a->max_n, CACHE_TILE) * a->batch * a->q_per_seq > INT32_MAX) return CSA2_ERR_UNSUPPORTED;   // tiles too
     if (!a->kv_offsets || !a->codes || !a->scales || !a->q || !a->out) return CSA2_ERR_INVALID_ARG;
     if (!(a->sm_scale - a->sm_scale == 0.0f)) return CSA2_ERR_INVALID_ARG;          // finite
     if (!aligned(a->codes, 16) || !aligned(a->scales, 16) || !aligned(a->q, 16) || !aligned(a->out, 16) ||

@@ -28,7 +28,7 @@ __device__ __forceinline__ int visible_positions(const CacheParams& p, int row) 
     const int b = p.q_per_seq == 1 ? row : row / p.q_per_seq;
     int n = static_cast<int>(max(static_cast<int64_t>(0), min(p.kv_offsets[b + 1] - p.kv_offsets[b], static_cast<int64_t>(p.max_n))));
     if (p.q_pos) {
-        const int64_t t = p.q_pos[b] + (row - b * p.q_per_seq) + 1;
+        const int64_t t = min(p.q_pos[b], int64_t(1) << 40) + (row - b * p.q_per_seq) + 1;
         n = static_cast<int>(min(static_cast<int64_t>(n), max(static_cast<int64_t>(0), t) >> (p.ratio - 1)));
     }
     return n;
@@ -372,7 +372,8 @@ __device__ __forceinline__ void put_query(const CacheParams& p, CacheSmem& sm, i
 #pragma unroll
         for (int i = 0; i < 16; ++i) n[i] >>= 3;
     }
-    if (lane == 0) sm.f[qb][h] = p.sm_scale * LOG2E * __uint_as_float(static_cast<uint32_t>(9 - k + 127) << 23);
+    if (lane == 0)                                          // a head with an infinity or NaN answers NaN
+        sm.f[qb][h] = top >= 0x7F80u ? NAN : p.sm_scale * LOG2E * __uint_as_float(static_cast<uint32_t>(9 - k + 127) << 23);
 }
 
 // Cache row of position pos of sequence b (RowMap::row with a plain load: the page table may
@@ -533,8 +534,9 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
             for (int t0 = tile; t0 < end; t0 += 32) {
                 int y = 0;                                  // each lane looks one tile's row up
                 if (t0 + lane < end) {
-                    const int64_t r0 = cache_row(p, b, off, v.pos(t0 + lane));
-                    const bool bad = r0 < 0 || r0 >= p.total_n;
+                    const int at = v.pos(t0 + lane);
+                    const int64_t r0 = cache_row(p, b, off, at);
+                    const bool bad = r0 < 0 || r0 + min(CACHE_TILE, v.n_vis - at) > p.total_n;
                     if (bad) atomicOr(err, ERR_DEVICE);
                     y = static_cast<int>(bad ? p.total_n : r0);      // past the end: reads zeros
                 }

@@ -291,6 +291,7 @@ append_rope_kernel(AppendParams p) {
     }
 
     double r = 1.0;
+    bool close = false;
     if (p.norm) {
         double ss = 0.0;
 #pragma unroll
@@ -305,6 +306,7 @@ append_rope_kernel(AppendParams p) {
             r = r0 * fma(-0.5 * a * r0, r0, 1.5);
         } else {
             r = 1.0 / sqrt(a);
+            close = true;                                   // and no fp32 products
         }
     }
 
@@ -312,10 +314,9 @@ append_rope_kernel(AppendParams p) {
     {
         const float rf = static_cast<float>(r);
         float y[16];
-        bool close = false;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            y[j] = x[j] * (w[j] * rf);
+            y[j] = (x[j] * rf) * w[j];                      // (x r stays below sqrt(512), whatever w is)
             close |= ((__float_as_uint(y[j]) - 0x7FFCu) & 0xFFFFu) <= 8u;
         }
         if (p.norm && __any_sync(0xFFFFFFFFu, close)) {

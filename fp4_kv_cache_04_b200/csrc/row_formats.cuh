@@ -31,6 +31,7 @@ __device__ __forceinline__ uint8_t nvfp4_group_hw(const uint16_t (&h)[16], uint2
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = max(top, static_cast<uint32_t>(h[i] & 0x7FFFu));
+    if (top >= 0x7F80u) return nvfp4_group(h, codes);      // infinities and NaN as there
     // amax / 6 by the same two steps: 8 bits over 2, against E4M3's midpoints of 5
     const float amax = bf16_bits_to_float(static_cast<uint16_t>(top)), q0 = amax * (1.0f / 6.0f);
     const uint32_t scale_code = e4m3x2_rn(fmaf(fmaf(-q0, 6.0f, amax), 1.0f / 6.0f, q0), 0.0f) & 0xFFu;
@@ -63,7 +64,12 @@ __device__ __forceinline__ void store_idx_row(float2 k, int lane, uint8_t* idx_k
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
     const float ks = amax / 448.0f;
-    const uint32_t c = ks > 0.0f ? e4m3x2_rn(k.x / ks, k.y / ks) : 0u;
+    uint32_t c = 0;
+    if (ks > 0.0f) {
+        // the minimum takes NaN (a NaN value, or inf / inf) to 448
+        const float q0 = k.x / ks, q1 = k.y / ks;
+        c = e4m3x2_rn(copysignf(fminf(fabsf(q0), 448.0f), q0), copysignf(fminf(fabsf(q1), 448.0f), q1));
+    }
     reinterpret_cast<uint16_t*>(idx_k)[lane] = static_cast<uint16_t>(c);
     if (lane == 0) *idx_kscale = ks;
 }

@@ -419,7 +419,7 @@ csa2_status csa2_set_wait_limit(void* workspace, uint32_t polls, void* stream);
  * u and v being channels 2i, 2i+1 of those r (or i, i + r/2 with CSA2_ROPE_HALF).  The
  * angle is formed and reduced in 64 bits, so far positions lose nothing.
  * Norm: y = x * w / sqrt(mean(x^2) + eps) over the vector's `dim` channels (w = 1 when
- * `weight` is NULL), before the rotation.
+ * `weight` is NULL), before the rotation; csa2_norm_rope squares and sums in fp32.
  * ------------------------------------------------------------------------------- */
 #define CSA2_T_BF16 0
 #define CSA2_T_F16  1
@@ -520,7 +520,10 @@ csa2_status csa2_dequantize_kv(const uint8_t* codes, const uint8_t* scales, int6
  * the call is made for decode steps and for a few drafted tokens.
  * The logits use the bf16 query written as six base-8 digits of a per-head fixed point
  * (exact for elements above 2^-7 of the head's largest, else to 2^-16 of it) times the
- * stored FP4 rows, summed in fp32; P is rounded to f16 (2^-12) for P V, summed in fp32. */
+ * stored FP4 rows, summed in fp32; P is rounded to f16 (2^-11) for P V, summed in fp32.
+ * A head whose query holds an infinity or a NaN answers NaN.  A position whose row or page
+ * lies outside the cache reads as zeros and sets CSA2_ERR_DEVICE in the workspace header
+ * (csa2_check_device_status). */
 typedef struct csa2_cache_args {
     int32_t batch;              /* B >= 1                                               */
     int32_t q_per_seq;          /* queries per sequence, 1 .. 65536                     */

@@ -135,3 +135,16 @@ def test_binding_refuses_host_tensors(csa2):
         csa2.rope_args(x=x, out=x)
     with pytest.raises(ValueError):
         csa2.rope_args(x=x, out=x[:1])
+
+
+def test_workspace_size_of_a_refused_call_is_zero(csa2):
+    for kw in (dict(max_n=0), dict(max_n=(1 << 63) - 1), dict(max_n=1 << 31), dict(batch=0), dict(q_per_seq=0),
+               dict(batch=(1 << 31) - 1, q_per_seq=65536), dict(window=-1), dict(sinks=-1)):
+        a = csa2.CacheArgs(**{**dict(batch=1, q_per_seq=1, ratio=1, max_n=1), **kw})
+        assert csa2.lib().csa2_cache_workspace_size(ctypes.byref(a)) == 0, kw
+
+
+def test_norm_rope_strides_beyond_64_bits_are_seen_to_overlap_or_not(csa2):
+    """(rows - 1) * stride passes 2^63: the heads would lie between the rows."""
+    far = 1 << 62
+    assert _rope(csa2, rows=1 << 20, heads=2, out_row_stride=far, out_head_stride=far) == 1

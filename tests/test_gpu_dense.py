@@ -236,6 +236,45 @@ def test_append_rope_rounds_like_the_quantiser_everywhere(csa2):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_append_not_finite_values_keep_the_quantiser_s_codes(csa2):
+    """Infinities and NaN: the FP4 row of append_kv; indexer codes of 448 (126) with the value's sign,
+    NaN counting as positive, against the largest of the others."""
+    inf, nan = math.inf, math.nan
+    x = torch.randn(6, 512, generator=gen(40), device=DEV).to(BF)
+    x[0, 3], x[1, 20], x[2, 37], x[3, :16], x[4, 500:], x[5, 64] = inf, -inf, nan, nan, -nan, 3e38
+    proj = torch.full((6, 64), 1.0, device=DEV)
+    proj[0, 3], proj[1, 4], proj[2, 5], proj[3, 6:8], proj[4, :] = nan, inf, -inf, torch.tensor([448.0, -1e-9], device=DEV), nan
+    want = torch.full((6, 64), 126, dtype=torch.uint8)         # 1 / (1 / 448) = 448
+    want[1:3] = 0                                              # 1 / inf = 0
+    want[1, 4], want[2, 5] = 126, 126                          # inf / inf = NaN
+    want[3], want[3, 6], want[3, 7] = 0x38, 126, 0x80          # 1.0, 448, -0
+    want[4] = 0                                                # nothing but NaN: so is the scale
+    caches = [blank_cache(6) for _ in range(2)]
+    offs, pos = torch.arange(7, device=DEV), torch.zeros(6, dtype=torch.int64, device=DEV)
+    c, s, ik, iks = caches[0]
+    csa2.append_kv(x, proj, offs[:6].contiguous(), c, s, ik, iks)
+    c2, s2, ik2, iks2 = caches[1]
+    csa2.append_rope(csa2.append_args(latent=x, pos=pos, codes=c2, scales=s2, kv_offsets=offs, norm=False, idx_proj=proj,
+                                      idx_k=ik2, idx_kscale=iks2))
+    for a, b in zip(*caches):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert torch.equal(ik.cpu(), want)
+    assert iks.tolist()[0] == np.float32(1) / np.float32(448) and iks.tolist()[1:3] == [inf, inf] and iks[4].isnan()
+
+
+@pytest.mark.parametrize("gain,wgain", [(1e-25, 1.0), (1e37, 1.0), (1e-18, 1e25), (1e18, 1e-20), (1.0, 1e30)])
+def test_append_rope_far_magnitudes(csa2, gain, wgain):
+    """fp32 latents whose squares, or whose weights times 1 / rms, leave the range of fp32."""
+    x = torch.randn(9, 512, generator=gen(41), device=DEV) * gain
+    w = (torch.rand(512, generator=gen(42), device=DEV) + 0.5) * wgain
+    pos, offs, f = torch.zeros(9, dtype=torch.int64, device=DEV), torch.arange(10, device=DEV), freqs(64)
+    c, s, _, _ = blank_cache(9)
+    csa2.append_rope(csa2.append_args(latent=x, pos=pos, codes=c, scales=s, kv_offsets=offs, weight=w, eps=0.0, inv_freq=f))
+    y = turned(normed(x.double(), w, 0.0), pos, f)
+    wc, ws = O.quantize_rows(O.f64_to_bf16(y.cpu().numpy()))
+    assert np.array_equal(c.cpu().numpy(), wc) and np.array_equal(s.cpu().numpy(), ws)
+
+
 def test_append_rope_skips_and_reports_what_lies_outside(csa2):
     lat = torch.randn(6, 512, generator=gen(8), device=DEV).to(BF)
     table = torch.tensor([[0, 1], [2, 9], [-1, 3]], dtype=torch.int32, device=DEV)     # page 9 of 4, page -1
@@ -492,6 +531,82 @@ def test_attend_cache_bad_page_is_reported(csa2):
         kv = rows64(codes, scales)[torch.arange(300, device=DEV) % 128 + torch.tensor([2, 3, 0], device=DEV)[torch.arange(300, device=DEV) // 128] * 128]
         w = torch.softmax(q[1].double() @ kv.T, -1) @ kv          # the other sequence is untouched by it
         assert (out[1].double() - w).norm() <= 4e-3 * w.norm()
+
+
+def test_attend_cache_rows_behind_the_packed_cache_are_reported(csa2):
+    """Offsets that reach past the last row, by whole tiles or inside one."""
+    codes, scales = make_cache(300, 1)
+    q = torch.randn(2, 16, 512, generator=gen(1), device=DEV).to(BF)
+    out = torch.empty(2, 16, 512, dtype=BF, device=DEV)
+    for last, status in ((300, 0), (301, 6), (384, 6), (700, 6)):
+        offs = torch.tensor([0, 100, last], device=DEV)
+        kw = dict(batch=2, max_n=600, kv_offsets=offs, codes=codes, scales=scales, q=q, out=out)
+        ws = csa2.alloc_workspace(csa2.cache_workspace_size(csa2.cache_args(**kw)))
+        csa2.attend_cache(csa2.cache_args(workspace=ws, **kw))
+        assert csa2.check_device_status(ws) == status
+        kv = rows64(codes, scales)[:100]
+        w = torch.softmax(q[0].double() @ kv.T, -1) @ kv          # the other sequence is untouched by it
+        assert (out[0].double() - w).norm() <= 4e-3 * w.norm()
+
+
+def test_attend_cache_query_position_without_end(csa2):
+    check_attend(csa2, [300, 20], q_per_seq=2, q_pos=[(1 << 63) - 1, -(1 << 63)], ratio=2)
+
+
+@pytest.mark.parametrize("n", [50, 5000])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_attend_cache_not_finite_query_stays_in_its_head(csa2, n, bad):
+    codes, scales = make_cache(n, 3)
+    q = torch.randn(1, 16, 512, generator=gen(4), device=DEV).to(BF)
+    outs = []
+    for value in (1.0, bad):
+        q[0, 5, 77] = value
+        out, lse = torch.empty(1, 16, 512, dtype=BF, device=DEV), torch.empty(1, 16, device=DEV)
+        kw = dict(batch=1, max_n=n, kv_offsets=torch.tensor([0, n], device=DEV), codes=codes, scales=scales, q=q, out=out,
+                  lse=lse, sm_scale=512 ** -0.5)
+        ws = csa2.alloc_workspace(csa2.cache_workspace_size(csa2.cache_args(**kw)))
+        csa2.attend_cache(csa2.cache_args(workspace=ws, **kw))
+        assert csa2.check_device_status(ws) == 0
+        outs.append((out, lse))
+    assert outs[1][0][0, 5].isnan().all() and outs[1][1][0, 5].isnan()
+    rest = [h for h in range(16) if h != 5]
+    assert torch.equal(outs[0][0][:, rest], outs[1][0][:, rest]) and torch.equal(outs[0][1][:, rest], outs[1][1][:, rest])
+
+
+def test_attend_cache_two_calls_at_once(csa2):
+    """Two streams, each with its own workspace and output."""
+    alone = check_attend(csa2, [4000, 31, 900], seed=6)[0]
+    codes, scales = make_cache(4931, 6)
+    offs = torch.tensor([0, 4000, 4031, 4931], device=DEV)
+    q = (torch.randn(3, 16, 512, generator=gen(8), device=DEV) * 2).to(BF)
+    jobs = []
+    for _ in range(2):
+        out = torch.zeros(4, 16, 512, dtype=BF, device=DEV)
+        kw = dict(batch=3, max_n=4000, kv_offsets=offs, codes=codes, scales=scales, q=q, out=out[:3], sm_scale=512 ** -0.5)
+        ws = csa2.alloc_workspace(csa2.cache_workspace_size(csa2.cache_args(**kw)))
+        jobs.append((torch.cuda.Stream(), csa2.cache_args(workspace=ws, **kw), out))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, a, _ in jobs:
+            csa2.attend_cache(a, stream=s)
+    torch.cuda.synchronize()
+    for _, _, out in jobs:
+        assert torch.equal(out[:3], alone[:3])
+
+
+def test_argument_blocks_let_their_tensors_go(csa2):
+    """A block that is dropped frees what it points at, without waiting for the cycle collector."""
+    import gc
+    gc.collect()
+    gc.disable()
+    try:
+        x = torch.zeros(1, 16, 512, dtype=BF, device=DEV)
+        before = torch.cuda.memory_allocated()
+        for _ in range(3):
+            csa2.norm_rope(csa2.rope_args(x=x, out=torch.empty_like(x)))
+        assert torch.cuda.memory_allocated() == before
+    finally:
+        gc.enable()
 
 
 # ------------------------------------------------------------------ together
