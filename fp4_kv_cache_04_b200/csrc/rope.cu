@@ -72,7 +72,8 @@ __device__ __forceinline__ void store8(typename Elem<T>::type* p, const float (&
     }
 }
 
-// Queries.  A block takes rows_per_block tokens: first their cos / sin tables (one per
+// Queries; bound by HBM (in + out once: 36 us for 4,096 x 16 fp32 vectors of 512 in and bf16
+// out, 5.6 TB/s) or, for a step's few tokens, by the launch.  A block takes rows_per_block tokens: first their cos / sin tables (one per
 // token, shared by its heads), then their vectors, `lanes` lanes (a power of two) per
 // vector and 8 channels per lane and item.  The half-split pairing reaches across lanes,
 // so there the vector goes through shared memory once.
@@ -237,7 +238,9 @@ __device__ __forceinline__ float load1(const typename Elem<T>::type* p) {
 // the fp32 one (2^-43); x * w * r in fp32 (off by 3 units at most), and again in 64 bits by
 // the whole warp where one of its 512 results lies within 4 units of a bf16 rounding border
 // (1 token in 14); the rotated channels in 64 bits throughout, a pair per lane and turn,
-// handed to their group's lane through shared memory.
+// handed to their group's lane through shared memory.  Bound by instructions and their
+// latencies (870 a token, issue slots 48 % busy; 64-bit throughout it took 21 us): 8,192
+// tokens ~11 us, 64 tokens 5.6 us in a graph with their read-back.
 template <int TI>
 __global__ void __launch_bounds__(32 * AR_WARPS)
 append_rope_kernel(AppendParams p) {
@@ -369,29 +372,27 @@ append_rope_kernel(AppendParams p) {
     p.scales[row * ROW_SCALES + lane] = sc;
 
     if (!p.idx_proj) return;
-    // indexer row: lane l holds values 2l, 2l+1 (a pair of the interleaved rotation)
+    // indexer row: lane l holds values 2l, 2l+1 (a pair of the interleaved rotation); turned in 64
+    // bits and rounded once to fp32, since its E4M3 codes change by whole steps too
     float2 k = *reinterpret_cast<const float2*>(p.idx_proj + i * p.idx_stride + 2 * lane);
     const int ip = p.idx_rope_dim / 2, k0 = 2 * lane - (IDX_DIM - p.idx_rope_dim);
     if (ip) {
+        const int pair = p.half ? lane : k0 >> 1;           // the one this lane turns by
+        const double2 a = pair >= 0 && pair < ip ? turn_cos_sin(turn_fraction(pos, p.idx_inv_freq[pair])) : make_double2(1.0, 0.0);
+        const double u = static_cast<double>(k.x), v = static_cast<double>(k.y);
         if (!p.half) {
-            float s = 0.0f, c = 1.0f;
-            if (k0 >= 0) sincospif(2.0f * static_cast<float>(turn_fraction(pos, p.idx_inv_freq[k0 >> 1])), &s, &c);
-            k = make_float2(k.x * c - k.y * s, k.y * c + k.x * s);
+            k = make_float2(static_cast<float>(fma(u, a.x, -(v * a.y))), static_cast<float>(fma(v, a.x, u * a.y)));
         } else {
             float out[2];
 #pragma unroll
             for (int d = 0; d < 2; ++d) {
                 const int kk = k0 + d;
                 const bool second = kk >= ip;
-                const int partner = (IDX_DIM - p.idx_rope_dim) + (kk < 0 ? 0 : second ? kk - ip : kk + ip);
-                const float o0 = __shfl_sync(0xFFFFFFFFu, k.x, partner >> 1);
-                const float o1 = __shfl_sync(0xFFFFFFFFu, k.y, partner >> 1);
-                const float other = (partner & 1) ? o1 : o0, me = d ? k.y : k.x;
-                float s = 0.0f, c = 1.0f;
-                if (kk >= 0)
-                    sincospif(2.0f * static_cast<float>(turn_fraction(pos, p.idx_inv_freq[second ? kk - ip : kk])), &s,
-                              &c);
-                out[d] = second ? me * c + other * s : me * c - other * s;
+                const int at = kk < 0 ? 0 : second ? kk - ip : kk, partner = (IDX_DIM - p.idx_rope_dim) + (second ? at : at + ip);
+                const double c = __shfl_sync(0xFFFFFFFFu, a.x, at), s = __shfl_sync(0xFFFFFFFFu, a.y, at);
+                const float o0 = __shfl_sync(0xFFFFFFFFu, k.x, partner >> 1), o1 = __shfl_sync(0xFFFFFFFFu, k.y, partner >> 1);
+                const double other = static_cast<double>((partner & 1) ? o1 : o0), me = d ? v : u;
+                out[d] = kk < 0 ? (d ? k.y : k.x) : static_cast<float>(second ? fma(me, c, other * s) : fma(me, c, -(other * s)));
             }
             k = make_float2(out[0], out[1]);
         }

@@ -461,8 +461,8 @@ csa2_status csa2_norm_rope(const csa2_rope_args* a, void* stream);
  *   y = rope(norm(latent[i]), pos[i]) rounded once to bf16, then the csa2_quantize_kv rule
  * (the sum, the norm, the angle and the products are carried far enough that the rounding
  * to bf16 is that of the real number), written at position pos[i] of sequence seq[i].
- * With idx_proj the token's indexer row is its 64 fp32 values, rotated when idx_rope_dim >
- * 0, in the format of csa2_append_kv.
+ * With idx_proj the token's indexer row is its 64 fp32 values, rotated (and rounded once to
+ * fp32) when idx_rope_dim > 0, in the format of csa2_append_kv.
  *   - A token with pos < 0 is padding: nothing is written for it.
  *   - A token whose sequence, position or page lies outside the cache is skipped and, when
  *     workspace is given, sets CSA2_ERR_DEVICE in its header (csa2_check_device_status).

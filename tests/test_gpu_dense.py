@@ -202,6 +202,26 @@ def test_append_rope_rows_are_exact(csa2, src, r, ri, half, norm, paged, idx, cu
     assert torch.equal(ik, want[2]) and torch.equal(iks, want[3])
 
 
+@pytest.mark.parametrize("ri,half", [(64, False), (64, True), (32, False), (6, True), (30, True)])
+def test_append_rope_indexer_rows_are_exact(csa2, ri, half):
+    """The real rotation rounded once to fp32, then the plain append's scale and codes: equal, over
+    half a million values."""
+    n = 8192
+    g = gen(50 + ri)
+    lat = torch.zeros(n, 512, dtype=BF, device=DEV)
+    proj = torch.randn(n, 64, generator=g, device=DEV)
+    pos = torch.randperm(1 << 17, generator=g, device=DEV)[:n]
+    seq, offs = torch.zeros(n, dtype=torch.int32, device=DEV), torch.tensor([0, 1 << 17], device=DEV)
+    codes, scales, ik, iks = blank_cache(1 << 17)
+    csa2.append_rope(csa2.append_args(latent=lat, pos=pos, seq=seq, codes=codes, scales=scales, kv_offsets=offs, norm=False,
+                                      half=half, idx_proj=proj, idx_inv_freq=freqs(ri), idx_k=ik, idx_kscale=iks))
+    k = turned(proj.double(), pos, freqs(ri), half).float().cpu().numpy()
+    ks = np.abs(k).max(-1) / np.float32(448)
+    assert ks.dtype == np.float32 and np.array_equal(iks[pos].cpu().numpy(), ks)
+    want = torch.from_numpy(k / ks[:, None]).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert torch.equal(ik[pos].cpu(), want)
+
+
 def test_append_rope_is_append_kv_without_norm_and_rotation(csa2):
     n = 70
     lat = torch.randn(n, 512, generator=gen(5), device=DEV).to(BF)
