@@ -222,7 +222,7 @@ __device__ __forceinline__ double2 turn_cos_sin(double t) {
 }
 
 // 72 registers a thread: an SM holds 7 blocks of 4 warps, or 3 of 8.  8,192 tokens (and their
-// read-back) take 15.1 us with 4, 15.2 with 2, 16.3 with 8.
+// read-back) take 14.8 us with 4, 14.9 with 2, 15.8 with 8.
 constexpr int AR_WARPS = 4;
 
 template <int T>
@@ -239,8 +239,9 @@ __device__ __forceinline__ float load1(const typename Elem<T>::type* p) {
 // the whole warp where one of its 512 results lies within 4 units of a bf16 rounding border
 // (1 token in 14); the rotated channels in 64 bits throughout, a pair per lane and turn,
 // handed to their group's lane through shared memory.  Bound by instructions and their
-// latencies (870 a token, issue slots 48 % busy; 64-bit throughout it took 21 us): 8,192
-// tokens ~11 us, 64 tokens 5.6 us in a graph with their read-back.
+// latencies (900 a token, issue slots half busy; what a token loads is asked for before its
+// norm, which is worth 0.6 us; 64-bit throughout it took 21 us): 8,192 tokens ~10 us, 64 tokens
+// 5.6 us in a graph with their read-back.
 template <int TI>
 __global__ void __launch_bounds__(32 * AR_WARPS)
 append_rope_kernel(AppendParams p) {
@@ -273,6 +274,14 @@ append_rope_kernel(AppendParams p) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) w[j] = 1.0f;
     }
+    // asked for now, used behind the norm
+    float freq = lane < p.rope_dim / 2 ? p.inv_freq[lane] : 0.0f;
+    const int ip = p.idx_proj ? p.idx_rope_dim / 2 : 0, k0 = 2 * lane - 2 * (IDX_DIM / 2 - ip);
+    const int pair = p.half ? lane : k0 >> 1;               // the indexer row's one that this lane turns by
+    float2 k = make_float2(0.0f, 0.0f);
+    float idx_freq = 0.0f;
+    if (p.idx_proj) k = *reinterpret_cast<const float2*>(p.idx_proj + i * p.idx_stride + 2 * lane);
+    if (pair >= 0 && pair < ip) idx_freq = p.idx_inv_freq[pair];
     if (pos < 0) return;
     // the row's place: looked up here, on its way until the row is stored
     int64_t base = -1, end = 0, in_page = 0;               // packed: first row and length; paged: page
@@ -340,7 +349,8 @@ append_rope_kernel(AppendParams p) {
         const auto* xr = static_cast<const typename Elem<TI>::type*>(p.latent) + i * p.latent_stride + start;
         for (int k = lane; k < pairs; k += 32) {
             const int iu = p.half ? k : 2 * k, iv = p.half ? k + pairs : 2 * k + 1;
-            const double2 a = turn_cos_sin(turn_fraction(pos, p.inv_freq[k]));
+            if (k >= 32) freq = p.inv_freq[k];
+            const double2 a = turn_cos_sin(turn_fraction(pos, freq));
             double u = static_cast<double>(load1<TI>(xr + iu)), v = static_cast<double>(load1<TI>(xr + iv));
             if (p.norm) {
                 u *= p.weight ? static_cast<double>(p.weight[start + iu]) * r : r;
@@ -374,11 +384,8 @@ append_rope_kernel(AppendParams p) {
     if (!p.idx_proj) return;
     // indexer row: lane l holds values 2l, 2l+1 (a pair of the interleaved rotation); turned in 64
     // bits and rounded once to fp32, since its E4M3 codes change by whole steps too
-    float2 k = *reinterpret_cast<const float2*>(p.idx_proj + i * p.idx_stride + 2 * lane);
-    const int ip = p.idx_rope_dim / 2, k0 = 2 * lane - (IDX_DIM - p.idx_rope_dim);
     if (ip) {
-        const int pair = p.half ? lane : k0 >> 1;           // the one this lane turns by
-        const double2 a = pair >= 0 && pair < ip ? turn_cos_sin(turn_fraction(pos, p.idx_inv_freq[pair])) : make_double2(1.0, 0.0);
+        const double2 a = turn_cos_sin(turn_fraction(pos, idx_freq));
         const double u = static_cast<double>(k.x), v = static_cast<double>(k.y);
         if (!p.half) {
             k = make_float2(static_cast<float>(fma(u, a.x, -(v * a.y))), static_cast<float>(fma(v, a.x, u * a.y)));
