@@ -309,7 +309,7 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
 }
 
 // Next row at or after `row` that sees anything (whole warp; there is one).
-__device__ __forceinline__ int next_row(const CacheParams& p, int row) {
+__device__ __noinline__ int next_row(const CacheParams& p, int row) {
     const int rows = p.batch * p.q_per_seq;
     for (; row < rows; row += 32) {
         const int r = row + (threadIdx.x & 31);
@@ -347,10 +347,24 @@ __device__ __forceinline__ void list_rows(const CacheParams& p, CacheSmem& sm, i
     }
 }
 
+// The six octal digits (each plus 4) of rint(v), |v| < 2^16, in the low six nibbles.
+__device__ __forceinline__ uint32_t spread_digits(float v) {
+    uint32_t x = __float_as_uint(v + 12582912.0f) - 0x4B400000u + 0x24924u;      // 1.5 2^23: rounds to an integer
+    x += 7 * (x & 0x3FE00u);                                // digits 3 .. 5 up by 3 bits
+    x += x & 0x1F81F8u;                                     // 1, 2, 4 and 5 by 1
+    x += x & 0x380380u;                                     // 2 and 5 by 1
+    return x;
+}
+
+// E2M1 codes of four digits, a byte each: -4 .. 3 looked up.
+__device__ __forceinline__ uint32_t digit_codes(uint32_t nibbles) { return __byte_perm(0x0A0C0D0Eu, 0x05040200u, nibbles); }
+
 // Head h of a row's query as six balanced base-8 digits: n = rint(q 2^k), 2^15 <= |n| <
 // 2^16 for the head's largest element, n = sum_d e_d 8^d with e_d in -4 .. 3, every one of
 // which E2M1 holds.  Adding 4 to every digit (0o444444) makes them plain octal digits.
-// One warp, lane l holds channels 16 l .. + 15.
+// One warp, lane l holds channels 16 l .. + 15.  Not inlined: one copy for all the warps that
+// come here, as what a launch runs once is bound by fetching its code (3 copies: 52 us for 64
+// rows of 4,096 positions, one 46.6).
 struct QueryHead {
     uint4 a, b;
 };
@@ -360,7 +374,7 @@ __device__ __forceinline__ QueryHead load_query(const CacheParams& p, int row, i
     return QueryHead{src[0], src[1]};
 }
 
-__device__ __forceinline__ void put_query(const CacheParams& p, CacheSmem& sm, int qb, int h, const QueryHead& v) {
+__device__ __noinline__ void put_query(float sm_scale, CacheSmem& sm, int qb, int h, const QueryHead v) {
     const int lane = threadIdx.x & 31;
     const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
     uint32_t top = 0;                                       // largest magnitude, as bf16 bits
@@ -370,33 +384,31 @@ __device__ __forceinline__ void put_query(const CacheParams& p, CacheSmem& sm, i
     const int e = static_cast<int>(top >> 7) - 127;         // largest in [2^e, 2^(e+1))
     const int k = min(15 - e, 126);
     const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-    uint32_t n[16];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        n[2 * i] = static_cast<uint32_t>(__float2int_rn(__uint_as_float(w[i] << 16) * up) + 0x24924);
-        n[2 * i + 1] = static_cast<uint32_t>(__float2int_rn(__uint_as_float(w[i] & 0xFFFF0000u) * up) + 0x24924);
-    }
     uint8_t* base = sm.q[qb] + (lane >> 4) * AC_QPANEL + h * 128 + ((((lane & 15) >> 1) ^ (h & 7)) << 4) + (lane & 1) * 8;
-#pragma unroll 1
-    for (int d = 0; d < AC_DIGITS; ++d) {                   // row 16 d + h
-        uint32_t out[2];
+    uint32_t out[2][AC_DIGITS];                             // [half][digit]: channels 8 half .. + 7, 4 bits each
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {                       // channels 8 j .. + 7: 4 bytes
-            uint32_t even = 0, odd = 0;
+    for (int j = 0; j < 2; ++j) {
+        uint32_t lo[4], hi[4];                              // channels 2 i, 2 i + 1: bytes of digits 0 .. 3, 4 and 5
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                even |= (n[8 * j + 2 * i] & 7u) << (4 * i);
-                odd |= (n[8 * j + 2 * i + 1] & 7u) << (4 * i);
-            }
-            // E2M1 codes of -4 .. 3 looked up four at a time
-            out[j] = __byte_perm(0x0A0C0D0Eu, 0x05040200u, even) | (__byte_perm(0x0A0C0D0Eu, 0x05040200u, odd) << 4);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t two = w[4 * j + i];
+            const uint32_t x = spread_digits(__uint_as_float(two << 16) * up), y = spread_digits(__uint_as_float(two & 0xFFFF0000u) * up);
+            lo[i] = digit_codes(x) + 16 * digit_codes(y);
+            hi[i] = digit_codes(x >> 16) + 16 * digit_codes(y >> 16);
         }
-        *reinterpret_cast<uint2*>(base + d * HEADS * 128) = make_uint2(out[0], out[1]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) n[i] >>= 3;
+        // bytes [channel pair][digit] -> [digit][channel pair]
+        const uint32_t a0 = __byte_perm(lo[0], lo[1], 0x5140), a1 = __byte_perm(lo[2], lo[3], 0x5140);
+        const uint32_t b0 = __byte_perm(lo[0], lo[1], 0x7362), b1 = __byte_perm(lo[2], lo[3], 0x7362);
+        const uint32_t c0 = __byte_perm(hi[0], hi[1], 0x5140), c1 = __byte_perm(hi[2], hi[3], 0x5140);
+        out[j][0] = __byte_perm(a0, a1, 0x5410), out[j][1] = __byte_perm(a0, a1, 0x7632);
+        out[j][2] = __byte_perm(b0, b1, 0x5410), out[j][3] = __byte_perm(b0, b1, 0x7632);
+        out[j][4] = __byte_perm(c0, c1, 0x5410), out[j][5] = __byte_perm(c0, c1, 0x7632);
     }
+#pragma unroll
+    for (int d = 0; d < AC_DIGITS; ++d)                     // row 16 d + h
+        *reinterpret_cast<uint2*>(base + d * HEADS * 128) = make_uint2(out[0][d], out[1][d]);
     if (lane == 0)                                          // a head with an infinity or NaN answers NaN
-        sm.f[qb][h] = top >= 0x7F80u ? NAN : p.sm_scale * LOG2E * __uint_as_float(static_cast<uint32_t>(9 - k + 127) << 23);
+        sm.f[qb][h] = top >= 0x7F80u ? NAN : sm_scale * LOG2E * __uint_as_float(static_cast<uint32_t>(9 - k + 127) << 23);
 }
 
 // Cache row of position pos of sequence b (RowMap::row with a plain load: the page table may
@@ -515,17 +527,58 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
     int it = 0, rw = 0;
     int row = range.row, left = range.count, tile = range.tile;
 
-    // the first row's query, a head per warp
-    auto first_query = [&]() {
-        if (range.count > 0) {
-            const QueryHead v = load_query(p, range.row, warp);
-            if (warp == AC_Q_WARP) list_rows(p, sm, range.row, static_cast<int64_t>(range.tile) + range.count);
-            put_query(p, sm, 0, warp, v);
-            fence_proxy_async_smem();
+    // the producer's copies: tile `it` from cache row y on, into its stage
+    uint64_t policy;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    auto copy_tile = [&](int y) {
+        const int st = it % AC_STAGES;
+        if (it >= AC_STAGES) {
+            wait(&sm.empty[st], it / AC_STAGES - 1);
+            wait(&sm.full[st], it / AC_STAGES - 1);         // landed, whoever gave up waiting for it
         }
-        __syncthreads();
-        tc_fence_after();
+        if (limit) {
+            uint8_t* dst = sm.stage[st];
+            mbar_arrive_expect_tx(&sm.full[st], AC_STAGE_BYTES);
+            tma_load_stream(dst, &tm_codes, 0, y, &sm.full[st], policy);
+            tma_load_stream(dst + AC_CODE_BYTES / 2, &tm_codes, 128, y, &sm.full[st], policy);
+            tma_load_stream(dst + AC_CODE_BYTES, &tm_scales, 0, y, &sm.full[st], policy);
+            sm.issued[st] = it / AC_STAGES + 1;
+        }
     };
+    // tiles [t0, end) of a row; each lane looks one tile's row up
+    auto copy_tiles = [&](const RowView& v, int t0, int end) {
+        const int b = row / p.q_per_seq;
+        const int64_t off = p.kv_offsets[b];
+        for (; t0 < end; t0 += 32) {
+            int y = 0;
+            if (t0 + lane < end) {
+                const int at = v.pos(t0 + lane);
+                const int64_t r0 = cache_row(p, b, off, at);
+                const bool bad = r0 < 0 || r0 + min(CACHE_TILE, v.n_vis - at) > p.total_n;
+                if (bad) atomicOr(err, ERR_DEVICE);
+                y = static_cast<int>(bad ? p.total_n : r0);      // past the end: reads zeros
+            }
+            for (int i = 0; i < 32 && t0 + i < end; ++i, ++it) {
+                const int yi = __shfl_sync(0xFFFFFFFFu, y, i);
+                if (lane == 0) copy_tile(yi);
+                __syncwarp();
+            }
+        }
+    };
+
+    // the first row's query, a head per warp; the first tiles are on their way before
+    if (range.count > 0) {
+        const QueryHead v = load_query(p, range.row, warp);
+        if (warp == AC_TMA_WARP) {
+            const RowView r = row_view(p, row);
+            copy_tiles(r, tile, min(min(r.tiles, tile + left), tile + AC_STAGES));
+        }
+        if (warp == AC_Q_WARP) list_rows(p, sm, range.row, static_cast<int64_t>(range.tile) + range.count);
+        put_query(p.sm_scale, sm, 0, warp, v);
+        fence_proxy_async_smem();
+    }
+    __syncthreads();
+    tc_fence_after();
     // the following rows' ones: heads [h0, h1) by this warp, the next one's values on their way
     int h0 = 0, h1 = 0, next = range.row;
     bool asked = false;
@@ -539,7 +592,7 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
         for (int h = h0; h < h1; ++h) {
             const QueryHead v = ahead;
             if (h + 1 < h1) ahead = load_query(p, next, h + 1);
-            put_query(p, sm, qb, h, v);
+            put_query(p.sm_scale, sm, qb, h, v);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -548,61 +601,19 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
 
     if (warp == AC_TMA_WARP) {
         // ---- producer: runs ahead over the rows, AC_STAGES tiles at most
-        uint64_t policy;
-        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
-        auto load_row = [&](const RowView& v, bool first) {
+        while (left > 0) {
+            const RowView v = range_row(p, sm, rw, row);
             const int end = min(v.tiles, tile + left);
-            const int b = row / p.q_per_seq;
-            const int64_t off = p.kv_offsets[b];
-            for (int t0 = tile; t0 < end; t0 += 32) {
-                int y = 0;                                  // each lane looks one tile's row up
-                if (t0 + lane < end) {
-                    const int at = v.pos(t0 + lane);
-                    const int64_t r0 = cache_row(p, b, off, at);
-                    const bool bad = r0 < 0 || r0 + min(CACHE_TILE, v.n_vis - at) > p.total_n;
-                    if (bad) atomicOr(err, ERR_DEVICE);
-                    y = static_cast<int>(bad ? p.total_n : r0);      // past the end: reads zeros
-                }
-                for (int i = 0; i < 32 && t0 + i < end; ++i, ++it) {
-                    const int yi = __shfl_sync(0xFFFFFFFFu, y, i);
-                    // the first row's query is still being written: its barrier comes once the
-                    // ring is full or the row is loaded
-                    if (first && it == AC_STAGES) {
-                        first_query();
-                        first = false;
-                    }
-                    if (lane == 0) {
-                        const int st = it % AC_STAGES;
-                        if (it >= AC_STAGES) {
-                            wait(&sm.empty[st], it / AC_STAGES - 1);
-                            wait(&sm.full[st], it / AC_STAGES - 1);      // landed, whoever gave up waiting for it
-                        }
-                        if (limit) {
-                            uint8_t* dst = sm.stage[st];
-                            mbar_arrive_expect_tx(&sm.full[st], AC_STAGE_BYTES);
-                            tma_load_stream(dst, &tm_codes, 0, yi, &sm.full[st], policy);
-                            tma_load_stream(dst + AC_CODE_BYTES / 2, &tm_codes, 128, yi, &sm.full[st], policy);
-                            tma_load_stream(dst + AC_CODE_BYTES, &tm_scales, 0, yi, &sm.full[st], policy);
-                            sm.issued[st] = it / AC_STAGES + 1;
-                        }
-                    }
-                    __syncwarp();
-                }
-            }
-            if (first) first_query();
+            copy_tiles(v, rw ? tile : tile + it, end);      // the first row's first ones are on their way
             left -= end - tile;
             tile = 0;
             ++rw;
-        };
-        if (left > 0) load_row(row_view(p, row), true);
-        else first_query();
-        while (left > 0) load_row(range_row(p, sm, rw, row), false);
+        }
         if (lane == 0) {                                    // no copy may land after the CTA is gone
             for (int st = 0; st < AC_STAGES; ++st)
                 if (sm.issued[st]) mbar_wait(&sm.full[st], static_cast<uint32_t>((sm.issued[st] - 1) & 1), err);
         }
     } else {
-        first_query();
         if (warp >= AC_MMA_WARP) {
             h0 = (warp - AC_MMA_WARP) * 5;
             h1 = warp == AC_Q_WARP ? HEADS : h0 + 5;
