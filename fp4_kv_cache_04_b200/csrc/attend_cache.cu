@@ -1089,13 +1089,13 @@ CachePlan cache_plan(int64_t rows, int64_t max_n, int64_t window, int64_t sinks)
     }
     // Uncut, the busiest CTA has whole rows to do; cut, all have the same number of tiles, and the
     // join and the second row of most CTAs cost as much as 3 to 5 tiles.  Measured uncut / cut (us):
-    // 1 row of 2 tiles 10.9 / 13.4, of 4 14.6 / 13.5; 16 rows of 4 14.8 / 15.0, of 8 21.7 / 16.2; 64
-    // rows of 4 15.7 / 18.3, of 8 22.5 / 25.6, of 16 36.1 / 35.5; 300 rows of 4 35.7 / 39.3, of 8
-    // 56.5 / 54.9, of 16 96.6 / 82.0.
+    // 1 row of 2 tiles 10.9 / 12.3, of 4 14.6 / 12.7; 16 rows of 4 14.8 / 13.9, of 8 21.8 / 15.5; 64
+    // rows of 4 15.5 / 19.2, of 8 22.3 / 25.5, of 16 36.1 / 34.5; 300 rows of 4 36.2 / 37.9, of 8
+    // 56.8 / 52.9, of 16 97.5 / 80.5.
     CachePlan plan;
     const int64_t idle = (ceil_div(rows, CACHE_MAX_RANGES) * CACHE_MAX_RANGES - rows) * tiles;   // tile slots
     // long rows are always cut: their true lengths may lie far below max_n
-    plan.whole_rows = tiles <= 8 && idle <= (rows < 8 ? 3 * CACHE_MAX_RANGES : 680);
+    plan.whole_rows = tiles <= 8 && idle <= (rows < 32 ? 3 * CACHE_MAX_RANGES : 680);
     const int64_t most = plan.whole_rows ? rows : tiles >= CACHE_MAX_RANGES ? tiles : rows * tiles;
     plan.ranges = static_cast<int>(std::min<int64_t>(CACHE_MAX_RANGES, most));
     return plan;
