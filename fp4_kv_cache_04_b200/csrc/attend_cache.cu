@@ -25,12 +25,12 @@
 // softmax (thread = key, packed fp32), 12 TMA (4 stages of 36 KB), 13 and 14 scale words
 // and MMAs of even and odd tiles, 15 the next row's query (with 13, 14) and the empty rows.
 //
-// Measured (1.83 GHz): 1.72 us a tile and SM, 3,140 cycles, against 1,580 for its 37 KB of
+// Measured (1.83 GHz): 1.7 us a tile and SM, 3,140 cycles, against 1,580 for its 37 KB of
 // HBM: P V alone takes 1,850, the logits' MMAs hold the tensor pipe for 490 more, and the
 // softmax shares the issue slots (1,600 warp instructions a scheduler and tile).  1.07 M
-// positions of 8 sequences: 123 us (47 at HBM's rate); 64 ragged sequences of up to 8,192 in
-// pages: 59 us (15).  The first P is ready 8.4 us into the launch (range 2.3, query 5.2,
-// logits 7.4), a row's end costs 1.9 us, the join 7: these bound the short calls.
+// positions of 8 sequences: 118 us (47 at HBM's rate); 64 ragged sequences of up to 8,192 in
+// pages: 55 us (15).  The first P is ready ~8 us into the launch (range 2.3, query 5, logits
+// 7), a row's end costs 1.9 us, the join 3 to 7: these bound the short calls.
 #include <algorithm>
 
 #include "dense.cuh"
@@ -976,7 +976,7 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
 // partial 1 of the range it starts in and
 // partials 0 of the following ones, in that order: GROUPS groups of threads take every GROUPS-th
 // and are added up in group order.  Bound by latency (4.8 MB of partials from L2 at most):
-// ~7 us behind the ranges' end.
+// 3 to 7 us behind the ranges' end.
 constexpr int AJ_AHEAD = 2;
 constexpr int AJ_THREADS = 512;
 static_assert(AJ_THREADS >= CACHE_MAX_RANGES, "a thread per range");
