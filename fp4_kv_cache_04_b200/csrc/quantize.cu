@@ -20,6 +20,15 @@ namespace csa2 {
 
 namespace {
 
+// Round-to-nearest-even of a float64 value to bf16, through a round-to-odd float32
+// intermediate (16 spare bits make the second rounding exact).
+__device__ __forceinline__ uint16_t f64_to_bf16_rne(double m) {
+    float f = __double2float_rz(m);
+    if (static_cast<double>(f) != m) f = __uint_as_float(__float_as_uint(f) | 1u);
+    __nv_bfloat16 h = __float2bfloat16_rn(f);
+    return *reinterpret_cast<uint16_t*>(&h);
+}
+
 __device__ __forceinline__ void unpack8(const uint4& v, uint16_t (&h)[16], int base) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

@@ -221,6 +221,12 @@ __device__ __forceinline__ double2 turn_cos_sin(double t) {
     return make_double2(n == 1 || n == 2 ? -cc : cc, n >= 2 ? -ss : ss);
 }
 
+// A 64-bit result's bf16 value: rounded to fp32, then to bf16, to nearest even both.
+__device__ __forceinline__ uint16_t bf16_by_f32(double m) {
+    const __nv_bfloat16 h = __float2bfloat16_rn(__double2float_rn(m));
+    return *reinterpret_cast<const uint16_t*>(&h);
+}
+
 // 72 registers a thread: an SM holds 7 blocks of 4 warps, or 3 of 8.  8,192 tokens (and their
 // read-back) take 14.8 us with 4, 14.9 with 2, 15.8 with 8.
 constexpr int AR_WARPS = 4;
@@ -233,11 +239,13 @@ __device__ __forceinline__ float load1(const typename Elem<T>::type* p) {
 }
 
 // One warp per token, one lane per 16-channel group (as in quantize.cu).  The FP4 codes
-// change by a whole step at a border, so the bf16 value they are made of is the real
-// number's rounding: the sum of squares in 64 bits, 1/sqrt by one 64-bit Newton step from
+// change by a whole step at a border, so the value they are made of is defined to the bit: the
+// real number rounded to fp32, as the indexer row's values are, and that to bf16 (what a
+// program has that casts its fp32 or fp64 result; off by half a bf16 step and half an fp32
+// step at most).  The sum of squares in 64 bits, 1/sqrt by one 64-bit Newton step from
 // the fp32 one (2^-43); x * w * r in fp32 (off by 3 units at most), and again in 64 bits by
 // the whole warp where one of its 512 results lies within 4 units of a bf16 rounding border
-// (1 token in 14); the rotated channels in 64 bits throughout, a pair per lane and turn,
+// (1 token in 14; elsewhere both fp32 values round to the same bf16); the rotated channels in 64 bits throughout, a pair per lane and turn,
 // handed to their group's lane through shared memory.  Bound by instructions and their
 // latencies (900 a token, issue slots half busy; what a token loads is asked for before its
 // norm, which is worth 0.6 us; 64-bit throughout it took 21 us): 8,192 tokens ~10 us, 64 tokens
@@ -332,7 +340,7 @@ append_rope_kernel(AppendParams p) {
         if (p.norm && __any_sync(0xFFFFFFFFu, close)) {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                h[j] = f64_to_bf16_rne(static_cast<double>(x[j]) * (static_cast<double>(w[j]) * r));
+                h[j] = bf16_by_f32(static_cast<double>(x[j]) * (static_cast<double>(w[j]) * r));
         } else {
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
@@ -356,8 +364,8 @@ append_rope_kernel(AppendParams p) {
                 u *= p.weight ? static_cast<double>(p.weight[start + iu]) * r : r;
                 v *= p.weight ? static_cast<double>(p.weight[start + iv]) * r : r;
             }
-            turned[iu] = f64_to_bf16_rne(fma(u, a.x, -(v * a.y)));
-            turned[iv] = f64_to_bf16_rne(fma(v, a.x, u * a.y));
+            turned[iu] = bf16_by_f32(fma(u, a.x, -(v * a.y)));
+            turned[iv] = bf16_by_f32(fma(v, a.x, u * a.y));
         }
         __syncwarp();
         const int c0 = lane * GROUP - start;                // first channel of the lane among the rotated

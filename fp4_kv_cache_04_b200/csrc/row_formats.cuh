@@ -6,15 +6,6 @@
 
 namespace csa2 {
 
-// Round-to-nearest-even of a float64 value to bf16, through a round-to-odd float32
-// intermediate (16 spare bits make the second rounding exact).
-__device__ __forceinline__ uint16_t f64_to_bf16_rne(double m) {
-    float f = __double2float_rz(m);
-    if (static_cast<double>(f) != m) f = __uint_as_float(__float_as_uint(f) | 1u);
-    __nv_bfloat16 h = __float2bfloat16_rn(f);
-    return *reinterpret_cast<uint16_t*>(&h);
-}
-
 // E4M3 codes of lo (bits 0..7) and hi (8..15), to nearest even, saturating at 448.
 __device__ __forceinline__ uint32_t e4m3x2_rn(float lo, float hi) {
     uint16_t v;

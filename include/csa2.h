@@ -458,9 +458,10 @@ csa2_status csa2_norm_rope(const csa2_rope_args* a, void* stream);
 
 /* csa2_append_rope — the cache append of csa2_append_kv with norm and rotation of the
  * latent on the way, addressed by (sequence, position) instead of by row.  Token i's row is
- *   y = rope(norm(latent[i]), pos[i]) rounded once to bf16, then the csa2_quantize_kv rule
- * (the sum, the norm, the angle and the products are carried far enough that the rounding
- * to bf16 is that of the real number), written at position pos[i] of sequence seq[i].
+ *   y = rope(norm(latent[i]), pos[i]) rounded to fp32 and that to bf16, then the
+ * csa2_quantize_kv rule (the sum, the norm, the angle and the products are carried far
+ * enough that the fp32 value is the real number's rounding wherever the bf16 one depends on
+ * it), written at position pos[i] of sequence seq[i].
  * With idx_proj the token's indexer row is its 64 fp32 values, rotated (and rounded once to
  * fp32) when idx_rope_dim > 0, in the format of csa2_append_kv.
  *   - A token with pos < 0 is padding: nothing is written for it.
