@@ -396,7 +396,8 @@ append_rope_kernel(AppendParams p) {
         const double2 a = turn_cos_sin(turn_fraction(pos, idx_freq));
         const double u = static_cast<double>(k.x), v = static_cast<double>(k.y);
         if (!p.half) {
-            k = make_float2(static_cast<float>(fma(u, a.x, -(v * a.y))), static_cast<float>(fma(v, a.x, u * a.y)));
+            // the others stay as they are: times cos 0 and sin 0 an infinity would reach its neighbour
+            if (pair >= 0) k = make_float2(static_cast<float>(fma(u, a.x, -(v * a.y))), static_cast<float>(fma(v, a.x, u * a.y)));
         } else {
             float out[2];
 #pragma unroll

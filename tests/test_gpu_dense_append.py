@@ -76,3 +76,43 @@ def test_a_chunk_of_normed_and_rotated_tokens_is_exact(csa2, seed, half):  # noq
     y = turned(normed(lat.double(), w, float(np.float32(1e-6))), pos, freqs(r), half)
     want = row_of_fp32(y)
     assert torch.equal(scales, want[1]) and torch.equal(codes, want[0])
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("ri", [2, 32, 62])
+@pytest.mark.parametrize("far", [False, True])
+def test_indexer_channels_outside_the_rotation_are_copied(csa2, ri, half, far):  # noqa: F811
+    """Infinities, NaN and zeros of both signs beside finite values, in the channels that are not
+    turned: the codes and scales of append_kv.  The turned ones are finite and stand at position 0, or
+    are zeros at far positions."""
+    inf, nan, keep = float("inf"), float("nan"), 64 - ri
+    special = [inf, -inf, nan, -nan, 0.0, -0.0, 448.0, -1e-30]
+    n = len(special) ** 2
+    proj = torch.randn(n, 64, generator=gen(ri), device=DEV)
+    for i in range(n):                       # every pair of them, at an even and at an odd channel
+        at = i % (keep - 1)
+        proj[i, at], proj[i, at + 1] = special[i // len(special)], special[i % len(special)]
+        if not i % 3:
+            proj[i, :keep] = proj[i, :keep].nan_to_num(nan=-0.0, posinf=0.0, neginf=-0.0)
+    pos = torch.zeros(n, dtype=torch.int64, device=DEV)
+    if far:
+        proj[:, keep:] = 0.0
+        pos += torch.arange(n, device=DEV) * 1001 + 5
+    lat, rows = torch.zeros(n, 512, dtype=BF, device=DEV), torch.arange(n, device=DEV)
+    a, b = blank_cache(n), blank_cache(n)
+    csa2.append_kv(lat, proj, rows, *a)
+    # far: every page of sequence i is page i
+    table = rows.to(torch.int32).view(n, 1).repeat(1, 1000)
+    if far:
+        b = blank_cache(128 * n)
+        csa2.append_rope(csa2.append_args(latent=lat, pos=pos, codes=b[0], scales=b[1], page_table=table, page_rows=128, norm=False,
+                                          half=half, idx_proj=proj, idx_inv_freq=freqs(ri), idx_k=b[2], idx_kscale=b[3]))
+        b = [t[rows * 128 + pos % 128] for t in b]
+    else:
+        offs = torch.arange(n + 1, device=DEV)
+        csa2.append_rope(csa2.append_args(latent=lat, pos=pos, codes=b[0], scales=b[1], kv_offsets=offs, norm=False, half=half,
+                                          idx_proj=proj, idx_inv_freq=freqs(ri), idx_k=b[2], idx_kscale=b[3]))
+    assert torch.equal(a[2][:, :keep], b[2][:, :keep])
+    assert torch.equal(a[3].view(torch.int32), b[3].view(torch.int32))
+    if not far:
+        assert torch.equal(a[2], b[2])
