@@ -511,6 +511,7 @@ def cache_args(*, batch: int, max_n: int, kv_offsets: torch.Tensor, codes: torch
 
 
 def cache_workspace_size(args: CacheArgs) -> int:
+    """Bytes of workspace; one for the largest batch, max_n and window serves smaller calls."""
     return _lib.csa2_cache_workspace_size(ctypes.byref(args))
 
 

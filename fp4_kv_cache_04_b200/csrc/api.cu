@@ -79,7 +79,8 @@ WsLayout layer_layout(const csa2_layer_args* a) {
 
 bool valid_type(int32_t t) { return t == CSA2_T_BF16 || t == CSA2_T_F16 || t == CSA2_T_F32; }
 
-// Workspace of csa2_attend_cache: two partials for each range of the tile list.
+// Workspace of csa2_attend_cache: two partials for each range of the tile list, as many as a cut
+// list of that many tiles has (a smaller batch may be cut where a larger one is not).
 struct CacheLayout {
     CachePlan plan;
     size_t meta = 0, part = 0, total = 0;
@@ -94,8 +95,8 @@ CacheLayout cache_layout(const csa2_cache_args* a) {
     CacheLayout L;
     L.plan = cache_plan(static_cast<int64_t>(a->batch) * a->q_per_seq, a->max_n, a->window, a->sinks);
     L.meta = WS_HEADER;
-    L.part = L.meta + align_up(static_cast<size_t>(L.plan.ranges) * 2 * sizeof(int32_t), 256);
-    L.total = L.part + align_up(static_cast<size_t>(L.plan.ranges) * 2 * CACHE_PART_FLOATS * sizeof(float), 256);
+    L.part = L.meta + align_up(static_cast<size_t>(L.plan.room) * 2 * sizeof(int32_t), 256);
+    L.total = L.part + align_up(static_cast<size_t>(L.plan.room) * 2 * CACHE_PART_FLOATS * sizeof(float), 256);
     return L;
 }
 

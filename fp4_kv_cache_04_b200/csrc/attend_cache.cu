@@ -1096,8 +1096,8 @@ CachePlan cache_plan(int64_t rows, int64_t max_n, int64_t window, int64_t sinks)
     const int64_t idle = (ceil_div(rows, CACHE_MAX_RANGES) * CACHE_MAX_RANGES - rows) * tiles;   // tile slots
     // long rows are always cut: their true lengths may lie far below max_n
     plan.whole_rows = tiles <= 8 && idle <= (rows < 32 ? 3 * CACHE_MAX_RANGES : 680);
-    const int64_t most = plan.whole_rows ? rows : tiles >= CACHE_MAX_RANGES ? tiles : rows * tiles;
-    plan.ranges = static_cast<int>(std::min<int64_t>(CACHE_MAX_RANGES, most));
+    plan.room = static_cast<int>(std::min<int64_t>(CACHE_MAX_RANGES, tiles >= CACHE_MAX_RANGES ? tiles : rows * tiles));
+    plan.ranges = plan.whole_rows ? static_cast<int>(std::min<int64_t>(CACHE_MAX_RANGES, rows)) : plan.room;
     return plan;
 }
 

@@ -95,6 +95,7 @@ constexpr int CACHE_PART_FLOATS = 2 * HEADS + HEADS * D;
 struct CachePlan {
     int ranges;
     bool whole_rows;
+    int room;                 // ranges that the workspace has room for: >= ranges, and never less for more work
 };
 CachePlan cache_plan(int64_t rows, int64_t max_n, int64_t window, int64_t sinks);
 // Tensor maps over codes as [total_n][256] bytes (boxes of 128 rows x 128 bytes, 128-byte

@@ -148,3 +148,29 @@ def test_norm_rope_strides_beyond_64_bits_are_seen_to_overlap_or_not(csa2):
     """(rows - 1) * stride passes 2^63: the heads would lie between the rows."""
     far = 1 << 62
     assert _rope(csa2, rows=1 << 20, heads=2, out_row_stride=far, out_head_stride=far) == 1
+
+
+def test_workspace_of_a_larger_call_serves_smaller_ones(csa2):
+    """The size never falls as any of the sizes grows, also where whole rows are dealt out."""
+    def size(**kw):
+        a = csa2.CacheArgs(**{**dict(batch=1, q_per_seq=1, ratio=1, max_n=1), **kw})
+        return csa2.lib().csa2_cache_workspace_size(ctypes.byref(a))
+    lengths = [1, 128, 129, 256, 384, 512, 640, 768, 896, 1000, 1024, 1025, 1280, 5000, 18944, 20000, 1 << 20]
+    for window, sinks in ((0, 0), (1, 0), (128, 4), (700, 300), (4096, 4)):
+        table = [[size(batch=b, max_n=n, window=window, sinks=sinks) for n in lengths] for b in range(1, 301)]
+        assert all(x <= y for row in table for x, y in zip(row, row[1:]))
+        assert all(x <= y for a, b in zip(table, table[1:]) for x, y in zip(a, b))
+        assert [size(batch=12, q_per_seq=k, max_n=1000, window=window, sinks=sinks) for k in (1, 2, 5)] == \
+            [size(batch=12 * k, max_n=1000, window=window, sinks=sinks) for k in (1, 2, 5)]
+    for rows in (1, 30, 62, 64, 200):
+        for n in (300, 1000, 5000):
+            by_window = [size(batch=rows, max_n=n, window=w, sinks=4) for w in (1, 2, 128, 129, 500, 900, 4096, 0)]
+            by_sinks = [size(batch=rows, max_n=n, window=200, sinks=s) for s in (0, 1, 128, 129, 500, 4096)]
+            assert by_window == sorted(by_window) and by_sinks == sorted(by_sinks)
+    assert size(batch=1 << 20, max_n=1 << 20) <= 9.8e6
+
+
+def test_a_workspace_below_the_stated_size_is_refused(csa2):
+    for rows in (30, 32, 62, 64):
+        need = csa2.lib().csa2_cache_workspace_size(ctypes.byref(csa2.CacheArgs(batch=rows, q_per_seq=1, ratio=1, max_n=1024)))
+        assert _cache(csa2, batch=rows, max_n=1024, workspace_bytes=need - 1) == 3
