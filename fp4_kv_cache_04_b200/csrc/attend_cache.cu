@@ -524,6 +524,8 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
             atomicOr(err, ERR_TIMEOUT);
         }
     };
+    // Lanes leave a wait one by one: a __syncwarp() stands between it and an instruction that wants
+    // the whole warp at once (tensor memory, ldmatrix, barriers).
     // every role walks the range's rows by itself: it counts tiles, rw rows
     int it = 0, rw = 0;
     int row = range.row, left = range.count, tile = range.tile;
@@ -702,12 +704,14 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                 for (int i = 0; i < HEADS / 2; ++i) l2[i] = 0;
                 if (rw >= 2) wait(&sm.r_empty[rb], (rw >> 1) - 1);
                 if (warp == AC_SM_WARP && lane < HEADS) sm.minus_m[rb][lane] = 0.0f;     // the first tile sets it
+                __syncwarp();
                 named_barrier(BAR_MAX, 128);
                 for (int t = tile; t < end; ++t, ++it) {
                     const int st = it % AC_STAGES, buf = it & 1, base = v.pos(t);
                     const bool vis = visible(p, v, base + key);
                     const bool all = base + CACHE_TILE <= v.n_vis && (base >= v.w_beg || base + CACHE_TILE <= p.sinks);
                     wait(&sm.s_full[buf], it >> 1);
+                    __syncwarp();
                     tc_fence_after();
                     uint64_t s[HEADS / 2];                  // the digits' columns summed, two heads a pair
                     const uint32_t src = tm + (static_cast<uint32_t>(32 * quarter) << 16) + AT_S + AT_S_STEP * buf;
@@ -735,6 +739,7 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
 #pragma unroll
                     for (int h = 2; h < HEADS; h += 2) d = max3(d, x[h], x[h + 1]);
                     if (it >= 2) wait(&sm.p_empty[buf], (it >> 1) - 1);
+                    __syncwarp();
                     const bool first = t == tile;
                     const bool moved = vote_barrier(BAR_VOTE, 128, d > AC_GAP + AC_SHIFT || first);
                     if (moved) {
@@ -833,6 +838,7 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                     const int st = it % AC_STAGES, buf = it & 1;
                     const uint32_t sa = stage0 + st * AC_STAGE_BYTES, pa = p0 + buf * AC_P_BYTES;
                     if (!ready) wait(&sm.p_full[buf], it >> 1);
+                    __syncwarp();
                     // step ks + 1's operands are loaded while step ks is multiplied
                     uint32_t a[2][4], sc[2][4];
                     uint2 c[2][4];
@@ -898,6 +904,7 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                 float* part = p.part + static_cast<int64_t>(slot) * CACHE_PART_FLOATS;
                 const int rb = rw & 1;
                 wait(&sm.r_full[rb], rw >> 1);
+                __syncwarp();
                 if (kh) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) sm.x[wq][i][lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);

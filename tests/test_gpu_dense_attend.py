@@ -70,3 +70,32 @@ def test_one_workspace_serves_every_smaller_batch(csa2, max_n, batches):  # noqa
         for b in range(0, batch, 5):
             assert check_row(q[b], every[offs[b]:offs[b + 1]], 512 ** -0.5, out[b]) <= 1
         assert (out[batch:] == 7.0).all()
+
+
+@pytest.mark.parametrize("lens,window,q_per_seq", [([5000, 3, 0, 997], 0, 1), ([900, 130] * 40, 0, 1), ([9000, 700, 20], 1000, 3),
+                                                   ([3, 1] * 700, 0, 1)])
+def test_waits_that_give_up_anywhere_end_the_call(csa2, lens, window, q_per_seq):  # noqa: F811
+    """Bounds from one poll to many: each call ends, with the timeout flagged or with the result, and
+    leaves nothing behind for the next one."""
+    B, rows = len(lens), len(lens) * q_per_seq
+    codes, scales = make_cache(sum(lens), 8)
+    offs = torch.tensor([0] + lens).cumsum(0).to(DEV)
+    q = torch.randn(rows, 16, 512, generator=gen(9), device=DEV).to(BF)
+    outs = [torch.empty(rows, 16, 512, device=DEV) for _ in range(2)]
+    kw = dict(batch=B, q_per_seq=q_per_seq, max_n=max(lens), kv_offsets=offs, codes=codes, scales=scales, q=q, sm_scale=512 ** -0.5,
+              window=window, sinks=4)
+    if q_per_seq > 1:
+        kw["q_pos"] = torch.tensor([max(0, n - q_per_seq) for n in lens], device=DEV)
+    ws = csa2.alloc_workspace(csa2.cache_workspace_size(csa2.cache_args(out=outs[0], **kw)))
+    csa2.attend_cache(csa2.cache_args(out=outs[0], workspace=ws, **kw))
+    assert csa2.check_device_status(ws) == 0
+    a = csa2.cache_args(out=outs[1], workspace=ws, **kw)
+    for polls in (1, 2, 3, 5, 8, 13, 30, 60, 100, 200, 400, 1000, 3000, 10000):
+        outs[1].fill_(5.0)
+        csa2.set_wait_limit(ws, polls)
+        csa2.attend_cache(a)
+        status = csa2.check_device_status(ws)
+        assert status in (0, 5) and (status == 5 or torch.equal(outs[0], outs[1]))
+    csa2.set_wait_limit(ws, 0)
+    csa2.attend_cache(a)
+    assert csa2.check_device_status(ws) == 0 and torch.equal(outs[0], outs[1])
