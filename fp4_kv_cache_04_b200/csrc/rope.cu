@@ -270,14 +270,22 @@ append_rope_kernel(AppendParams p) {
         for (int j = 0; j < 8; ++j) x[8 * q + j] = a[j];
     }
     float w[16];
+    bool close = false;
     if (p.norm && p.weight) {
+        float top = 0.0f;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             float a[8];
             load8<CSA2_T_F32>(p.weight + lane * GROUP + 8 * q, a);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[8 * q + j] = a[j];
+            for (int j = 0; j < 8; ++j) {
+                w[8 * q + j] = a[j];
+                top = fmaxf(top, fabsf(a[j]));
+            }
         }
+        // x r below 2^-126 has lost bits in fp32: under such a weight they count, under smaller ones
+        // the result is below 2^-26, far from FP4's lowest border (2^-11)
+        close = top > 0x1p100f;
     } else {
 #pragma unroll
         for (int j = 0; j < 16; ++j) w[j] = 1.0f;
@@ -309,7 +317,6 @@ append_rope_kernel(AppendParams p) {
     }
 
     double r = 1.0;
-    bool close = false;
     if (p.norm) {
         double ss = 0.0;
 #pragma unroll

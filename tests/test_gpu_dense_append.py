@@ -116,3 +116,21 @@ def test_indexer_channels_outside_the_rotation_are_copied(csa2, ri, half, far): 
     assert torch.equal(a[3].view(torch.int32), b[3].view(torch.int32))
     if not far:
         assert torch.equal(a[2], b[2])
+
+
+@pytest.mark.parametrize("r", [0, 64])
+def test_weights_that_bring_back_what_fp32_loses(csa2, r):  # noqa: F811
+    """x / rms below fp32's normal range keeps 14 bits there, and a weight of 2^127 makes it count."""
+    n = 4096
+    g = gen(60)
+    x = torch.randn(n, 512, generator=g, device=DEV)
+    tiny = torch.zeros(512, dtype=torch.bool, device=DEV)
+    tiny[32:96], tiny[200:216] = True, True
+    x[:, tiny] = torch.randn(n, int(tiny.sum()), generator=g, device=DEV) * 2.0 ** -134
+    w = torch.rand(512, generator=g, device=DEV) + 0.5
+    w[tiny] *= 2.0 ** 127
+    codes, scales = append(csa2, x, weight=w, eps=1e-6, inv_freq=freqs(r))
+    y = turned(normed(x.double(), w, float(np.float32(1e-6))), torch.arange(n, device=DEV), freqs(r))
+    want = row_of_fp32(y)
+    assert (want[1][:, 2:6] > 0).any()
+    assert torch.equal(scales, want[1]) and torch.equal(codes, want[0])
