@@ -86,9 +86,9 @@ struct CacheLayout {
     size_t meta = 0, part = 0, total = 0;
 };
 
-// Positions of a row and rows are counted in 32 bits.
+// Positions of a row, up to its last tile's end, and rows are counted in 32 bits.
 bool cache_sizes_fit(const csa2_cache_args* a) {
-    return a->max_n <= INT32_MAX && static_cast<int64_t>(a->batch) * a->q_per_seq <= INT32_MAX;
+    return a->max_n <= INT32_MAX - (CACHE_TILE - 1) && static_cast<int64_t>(a->batch) * a->q_per_seq <= INT32_MAX;
 }
 
 CacheLayout cache_layout(const csa2_cache_args* a) {

@@ -530,7 +530,7 @@ typedef struct csa2_cache_args {
     int32_t q_per_seq;          /* queries per sequence, 1 .. 65536                     */
     int32_t ratio;              /* 1 or 2 (with q_pos)                                  */
     int32_t out_type;           /* CSA2_T_BF16 or CSA2_T_F32                            */
-    int64_t max_n;              /* host upper bound on every N_b (>= 1)                 */
+    int64_t max_n;              /* host upper bound on every N_b (1 .. 2^31-128)        */
     int64_t total_n;            /* rows of codes / scales (1 .. 2^31-1)                 */
     int64_t window;             /* 0: every position; else the last `window` ones       */
     int64_t sinks;              /* with window: first positions that stay visible       */

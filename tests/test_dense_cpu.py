@@ -174,3 +174,13 @@ def test_a_workspace_below_the_stated_size_is_refused(csa2):
     for rows in (30, 32, 62, 64):
         need = csa2.lib().csa2_cache_workspace_size(ctypes.byref(csa2.CacheArgs(batch=rows, q_per_seq=1, ratio=1, max_n=1024)))
         assert _cache(csa2, batch=rows, max_n=1024, workspace_bytes=need - 1) == 3
+
+
+def test_positions_whose_last_tile_ends_past_32_bits_are_refused(csa2):
+    """A tile's end is counted in 32 bits: a sequence may be that long where its pages repeat."""
+    last = (1 << 31) - 128
+    size = lambda n: csa2.lib().csa2_cache_workspace_size(ctypes.byref(csa2.CacheArgs(batch=1, q_per_seq=1, ratio=1, max_n=n)))  # noqa: E731
+    assert size(last) == size(1 << 20) and size(last + 1) == size((1 << 31) - 1) == 0
+    assert _cache(csa2, batch=1, max_n=last, workspace_bytes=256) == 3
+    for n in (last + 1, (1 << 31) - 1):
+        assert _cache(csa2, batch=1, max_n=n, workspace_bytes=256) == 2
