@@ -367,6 +367,14 @@ def _launch(fn, args, stream, where: str) -> None:
         raise Csa2Error(status, where)
 
 
+def _cache_rows(codes: torch.Tensor, scales: torch.Tensor) -> int:
+    """Rows of a cache: the first dimension of two matrices, also of a paged one (pages in turn)."""
+    _need(codes.dtype == torch.uint8 and scales.dtype == torch.uint8 and codes.dim() == 2 and scales.dim() == 2 and
+          codes.shape[1] == ROW_CODES and scales.shape[1] == ROW_SCALES and codes.shape[0] == scales.shape[0],
+          "codes uint8 [rows][256] and scales uint8 [rows][32]")
+    return codes.shape[0]
+
+
 def _vec(t: torch.Tensor | None, dtype, n: int, what: str) -> int | None:
     if t is None:
         return None
@@ -426,10 +434,7 @@ def append_args(*, latent: torch.Tensor, pos: torch.Tensor, codes: torch.Tensor,
     indexer rows."""
     n = latent.shape[0]
     _need(latent.dim() == 2 and latent.shape[1] == D, "latent is [n][512]")
-    _need(codes.dtype == torch.uint8 and scales.dtype == torch.uint8 and codes.dim() == 2 and scales.dim() == 2 and
-          codes.shape[1] == ROW_CODES and scales.shape[1] == ROW_SCALES and codes.shape[0] == scales.shape[0],
-          "codes uint8 [rows][256] and scales uint8 [rows][32]")
-    total = codes.shape[0]
+    total = _cache_rows(codes, scales)
     _need((kv_offsets is None) != (page_table is None), "either kv_offsets or page_table")
     if page_table is not None:
         _need(page_table.dtype == torch.int32 and page_table.dim() == 2, "page_table is int32 [batch][pages]")
@@ -496,8 +501,7 @@ def cache_args(*, batch: int, max_n: int, kv_offsets: torch.Tensor, codes: torch
     rows = batch * q_per_seq
     _need(q.dtype == torch.bfloat16 and q.numel() == rows * HEADS * D, "q is bf16 [batch * q_per_seq][16][512]")
     _need(out.numel() == rows * HEADS * D, "out is [batch * q_per_seq][16][512]")
-    _need(codes.dtype == torch.uint8 and scales.dtype == torch.uint8 and codes.shape[0] == scales.shape[0] and
-          codes.shape[-1] == ROW_CODES and scales.shape[-1] == ROW_SCALES, "codes uint8 [rows][256], scales uint8 [rows][32]")
+    _cache_rows(codes, scales)
     _need(page_table is None or (page_table.dtype == torch.int32 and page_table.dim() == 2 and
                                  page_table.shape[0] == batch), "page_table is int32 [batch][pages]")
     a = CacheArgs(batch, q_per_seq, ratio, TYPES.get(out.dtype, -1), max_n, codes.shape[0], window, sinks,

@@ -184,3 +184,15 @@ def test_positions_whose_last_tile_ends_past_32_bits_are_refused(csa2):
     assert _cache(csa2, batch=1, max_n=last, workspace_bytes=256) == 3
     for n in (last + 1, (1 << 31) - 1):
         assert _cache(csa2, batch=1, max_n=n, workspace_bytes=256) == 2
+
+
+@pytest.mark.parametrize("codes,scales", [((4, 128, 256), (4, 128, 32)), ((512, 256), (511, 32)), ((512, 256), (4, 128, 32)),
+                                          ((512, 2, 256), (512, 32)), ((256,), (32,))])
+def test_binding_refuses_a_cache_that_is_not_two_matrices(csa2, codes, scales):
+    """The first dimension counts rows: of a cache given as [pages][page_rows][256] it would count
+    pages, and the rows behind would be taken for missing ones."""
+    import torch
+    q = torch.zeros(1, 16, 512, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match=r"codes uint8 \[rows\]\[256\]"):
+        csa2.cache_args(batch=1, max_n=512, kv_offsets=torch.zeros(2, dtype=torch.int64), q=q, out=q,
+                        codes=torch.zeros(codes, dtype=torch.uint8), scales=torch.zeros(scales, dtype=torch.uint8))
