@@ -5,7 +5,8 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_dense import BF, DEV, FP, csa2, gen, make_cache, row_of, rows64, seen_positions, table_for  # noqa: F401
+from tests.test_gpu_dense import (BF, DEV, FP, blank_cache, csa2, freqs, gen, make_cache, row_of, rows64,  # noqa: F401
+                                  seen_positions, table_for, turned)
 
 pytestmark = pytest.mark.gpu
 
@@ -24,9 +25,10 @@ def check_row(q, kv, sm_scale, out, lse=None, out_type=None):
     q64 = fixed_point(q)
     s = q64 @ kv.T * sm_scale
     w = torch.softmax(s, -1)
-    # a logit: six digits' sums of eight MMA steps and five additions, about 54 roundings of 2^-23
-    # of partial sums that Cauchy-Schwarz bounds: 2^-17 in all.  It counts by the key's weight.
-    ds = 2.0 ** -17 * abs(sm_scale) * q64.norm(dim=-1, keepdim=True) * kv.norm(dim=-1)
+    # a logit: six digits' sums of eight MMA steps and five additions of them, 54 roundings of up to
+    # 2^-23 of partial sums; the digits' magnitudes add up to 3 |q| at most (4 = 8 - 4).  It counts
+    # by the key's weight.
+    ds = 54 * 3 * 2.0 ** -23 * abs(sm_scale) * (q64.abs() @ kv.abs().T)
     mean = (w * ds).sum(-1, keepdim=True)
     n_add = 2.0 ** -23 * (kv.shape[0] / 16 + 32)                # P V adds 16 positions per step
     want, a = w @ kv, kv.abs()
@@ -99,3 +101,180 @@ def test_waits_that_give_up_anywhere_end_the_call(csa2, lens, window, q_per_seq)
     csa2.set_wait_limit(ws, 0)
     csa2.attend_cache(a)
     assert csa2.check_device_status(ws) == 0 and torch.equal(outs[0], outs[1])
+
+
+def place(lens, page, seed):
+    """Offsets, page table (or None) and rows of a cache of these lengths."""
+    offs = torch.tensor([0] + lens).cumsum(0).to(DEV)
+    if not page:
+        return offs, None, max(1, sum(lens))
+    pages = max(1, max(-(-n // page) for n in lens))
+    return offs, table_for(len(lens), pages, len(lens) * pages + 3, seed), (len(lens) * pages + 3) * page
+
+
+def run_and_check(csa2, lens, q_of, page=0, window=0, sinks=0, q_per_seq=1, q_pos=None, ratio=1, sm_scale=512 ** -0.5, spread=1.0,  # noqa: F811
+                  out_type=FP, cache=None):
+    offs, table, total = place(lens, page, 5)
+    codes, scales = cache or make_cache(total, 6, spread)
+    rows, max_n = len(lens) * q_per_seq, max(1, max(lens))
+    q = q_of(rows).to(BF)
+    out, lse = torch.empty(rows, 16, 512, dtype=out_type, device=DEV), torch.empty(rows, 16, device=DEV)
+    attend(csa2, q, out, codes, scales, offs, max_n, q_per_seq=q_per_seq, window=window, sinks=sinks, ratio=ratio, sm_scale=sm_scale,
+           lse=lse, page_table=table, page_rows=page, q_pos=None if q_pos is None else torch.tensor(q_pos, device=DEV))
+    for r in range(rows):
+        b, i = divmod(r, q_per_seq)
+        p = seen_positions(lens[b], None if q_pos is None else q_pos[b] + i, ratio, window, sinks)
+        if not p.numel():
+            assert (out[r] == 0).all() and (lse[r] == -math.inf).all()
+            continue
+        at = row_of(torch.full_like(p, b), p, offs, table, page)
+        assert check_row(q[r], rows64(codes[at], scales[at]), sm_scale, out[r], lse[r]) <= 1, f"row {r}"
+
+
+def test_the_bound_sees_one_position_of_500():
+    """The check itself: float64 attention over one row more or less, or a row twice, is out of its bound."""
+    kv = rows64(*make_cache(501, 1))
+    q = torch.zeros(16, 512, dtype=BF, device=DEV)
+    out, lse = kv[:500].mean(0).expand(16, 512), torch.full((16,), math.log(500.0), device=DEV, dtype=torch.float64)
+    assert check_row(q, kv[:500], 0.1, out, lse, out_type=FP) <= 1
+    for other in (kv, kv[:499], kv[1:500], torch.cat([kv[:499], kv[:1]])):
+        assert check_row(q, other, 0.1, out, out_type=FP) > 2
+
+
+def normal(gain, seed=3):
+    return lambda rows: torch.randn(rows, 16, 512, generator=gen(seed), device=DEV) * gain
+
+
+# gain 0: every key weighs the same, and one key more or less of 500 is several times the bound
+@pytest.mark.parametrize("gain", [0.0, 0.3, 2.0])
+@pytest.mark.parametrize("window,sinks,page", [(0, 0, 0), (0, 0, 128), (130, 5, 256), (128, 0, 0), (1, 1, 0), (700, 300, 128)])
+def test_no_position_more_or_less(csa2, gain, window, sinks, page):  # noqa: F811
+    run_and_check(csa2, [513, 128, 1, 0, 129, 1300, 255, 384], normal(gain), page=page, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("ratio", [1, 2])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (200, 9)])
+def test_no_position_more_or_less_for_drafts(csa2, ratio, window, sinks):  # noqa: F811
+    run_and_check(csa2, [500, 260, 17, 0, 385], normal(0.0), window=window, sinks=sinks, q_per_seq=4, ratio=ratio,
+                  q_pos=[1, 260 * ratio - 4, 1000, 3, 380 * ratio])
+
+
+@pytest.mark.parametrize("n", [700, 5000])
+@pytest.mark.parametrize("by", [1e2, 1e4, 1e6])
+def test_a_channel_far_above_the_rest_of_its_query(csa2, n, by):  # noqa: F811
+    """The rest is held to 2^-16 of the largest, as documented: the reference has the same fixed point."""
+    def q_of(rows):
+        q = normal(1.0)(rows)
+        for h in range(16):
+            q[:, h, 32 * h + h] = by
+        return q
+    run_and_check(csa2, [n, 50], q_of, sm_scale=512 ** -0.5 / by ** 0.5)
+
+
+@pytest.mark.parametrize("gain,spread,sm_scale", [(2.0, 60.0, 512 ** -0.5), (20.0, 1.0, 512 ** -0.5), (2.0, 1.0, 1.0), (1e-30, 1.0, 1e30),
+                                                  (2.0, 0.004, 1.0), (1e30, 1.0, 1e-31), (3e38, 1.0, 1e-38)])
+def test_peaked_softmax_and_far_magnitudes(csa2, gain, spread, sm_scale):  # noqa: F811
+    run_and_check(csa2, [900, 3, 2500], lambda rows: normal(1.0)(rows).clamp(-1, 1) * gain, spread=spread, sm_scale=sm_scale)
+
+
+@pytest.mark.parametrize("falling", [False, True])
+def test_running_reference(csa2, falling):  # noqa: F811
+    """Tiles whose logits rise or fall throughout, for one head; the others see them in any order."""
+    n = 4096
+    codes, scales = make_cache(n, 12)
+    q = normal(2.0)(1)
+    order = torch.argsort(rows64(codes, scales) @ q[0, 3].to(BF).double(), descending=falling)
+    run_and_check(csa2, [n], lambda rows: q, cache=(codes[order].contiguous(), scales[order].contiguous()), sm_scale=0.25)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_a_step_of_a_dense_layer_each_operator_from_what_the_last_one_left(csa2, graph):  # noqa: F811
+    """Append, query, attention, rotation back and read-back of three steps, eager or as one captured
+    graph that is replayed on new inputs; each result against float64 of the operands that it had."""
+    g = gen(70)
+    B, page, r = 3, 128, 64
+    table = table_for(B, 5, 20, 3)
+    codes, scales, _, _ = blank_cache(20 * page)
+    lens = torch.tensor([126, 0, 511], device=DEV)
+    old = torch.cat([torch.arange(int(n), device=DEV) for n in lens])
+    seq = torch.repeat_interleave(torch.arange(B, device=DEV), lens).to(torch.int32)
+    csa2.append_rope(csa2.append_args(latent=torch.randn(old.numel(), 512, generator=g, device=DEV).to(BF), pos=old, seq=seq, codes=codes,
+                                      scales=scales, page_table=table, page_rows=page))
+    wq, wk, f = torch.rand(512, generator=g, device=DEV) + 0.5, torch.rand(512, generator=g, device=DEV) + 0.5, freqs(r)
+    proj, pos = torch.empty(B, 17 * 512, dtype=BF, device=DEV), torch.empty(B, dtype=torch.int64, device=DEV)
+    offs, rows = torch.zeros(B + 1, dtype=torch.int64, device=DEV), torch.empty(B, dtype=torch.int64, device=DEV)
+    q, out = torch.empty(B, 16, 512, dtype=BF, device=DEV), torch.empty(B, 16, 512, device=DEV)
+    back, got = torch.empty(B, 16, 512, dtype=BF, device=DEV), torch.empty(B, 512, dtype=BF, device=DEV)
+    new = csa2.append_args(latent=proj[:, 8192:], pos=pos, codes=codes, scales=scales, page_table=table, page_rows=page, weight=wk,
+                           inv_freq=f)
+    query = csa2.rope_args(x=proj[:, :8192].unflatten(1, (16, 512)), out=q, pos=pos, inv_freq=f, weight=wq)
+    kw = dict(batch=B, max_n=600, kv_offsets=offs, codes=codes, scales=scales, q=q, out=out, sm_scale=512 ** -0.5, page_table=table,
+              page_rows=page)
+    ws = csa2.alloc_workspace(csa2.cache_workspace_size(csa2.cache_args(**kw)))
+    every = csa2.cache_args(workspace=ws, **kw)
+    turn = csa2.rope_args(x=out, out=back, pos=pos, inv_freq=f, norm=False, inverse=True)
+
+    def step():
+        csa2.append_rope(new)
+        csa2.norm_rope(query)
+        csa2.attend_cache(every)
+        csa2.norm_rope(turn)
+        csa2.dequantize_kv(codes, scales, got, src_row=rows)
+
+    def inputs(k):
+        proj.copy_(torch.randn(B, 17 * 512, generator=gen(80 + k), device=DEV))
+        pos.copy_(lens + k)
+        offs[1:] = (pos + 1).cumsum(0)
+        rows.copy_(row_of(torch.arange(B, device=DEV), pos, None, table, page))
+
+    run = step
+    if graph:
+        inputs(0)
+        step()
+        torch.cuda.synchronize()
+        captured = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured):
+            step()
+        run = captured.replay
+    for k in range(3):
+        inputs(k)
+        run()
+        torch.cuda.synchronize()
+        assert csa2.check_device_status(ws) == 0
+        assert torch.equal(got.double(), rows64(codes[rows], scales[rows]))
+        for b in range(B):
+            p = torch.arange(int(pos[b]) + 1, device=DEV)
+            at = row_of(torch.full_like(p, b), p, None, table, page)
+            assert check_row(q[b], rows64(codes[at], scales[at]), 512 ** -0.5, out[b]) <= 1
+        want = turned(out.double(), pos, f, sign=-1.0)
+        # fp32 rotation 36 u32 of |u| + |v| <= 2 max, then one rounding to bf16
+        tol = 72 * 2.0 ** -24 * out.abs().amax(-1, keepdim=True) + 2.0 ** -8 * want.abs()
+        assert ((back.double() - want).abs() <= tol).all()
+
+
+def test_selected_attention_right_behind_the_append(csa2):  # noqa: F811
+    """csa2_attend launched behind the append of rows that it reads: as if the append had been waited for."""
+    n, B = 400, 4
+    offs = torch.arange(B + 1, device=DEV) * n
+    lat = torch.randn(B * n, 512, generator=gen(90), device=DEV).to(BF)
+    seq, pos = torch.arange(B, device=DEV).to(torch.int32).repeat_interleave(n), torch.arange(n, device=DEV).repeat(B)
+    q, swa = torch.randn(B, 16, 512, generator=gen(91), device=DEV).to(BF), torch.randn(B, 128, 512, generator=gen(92), device=DEV).to(BF)
+    topk = torch.full((B, 512), -1, dtype=torch.int32, device=DEV)
+    topk[:, :n] = torch.arange(n, device=DEV)
+    codes, scales, _, _ = blank_cache(B * n)
+    outs = []
+    new = csa2.append_args(latent=lat, pos=pos, seq=seq, codes=codes, scales=scales, kv_offsets=offs, inv_freq=freqs(64))
+    for wait in (True, False, False):
+        codes.fill_(0), scales.fill_(0)
+        out = torch.empty(B, 16, 512, device=DEV)
+        kw = dict(mode=csa2.MODE_REUSE, batch=B, q_per_seq=1, max_n=n, kv_offsets=offs, codes=codes, scales=scales, topk_idx=topk, q=q,
+                  swa_kv=swa, out=out, sm_scale=512 ** -0.5)
+        layer = csa2.layer_args(workspace=csa2.alloc_workspace(csa2.workspace_size(csa2.layer_args(**kw))), **kw)
+        torch.cuda.synchronize()
+        csa2.append_rope(new)
+        if wait:
+            torch.cuda.synchronize()
+        csa2.attend(layer)
+        outs.append(out)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
