@@ -1094,15 +1094,18 @@ CachePlan cache_plan(int64_t rows, int64_t max_n, int64_t window, int64_t sinks)
         const int64_t w = std::min(window, max_n), s = std::min(sinks, max_n);
         tiles = std::min(tiles, ceil_div(w, CACHE_TILE) + 1 + ceil_div(s, CACHE_TILE));
     }
-    // Uncut, the busiest CTA has whole rows to do; cut, all have the same number of tiles, and the
-    // join and the second row of most CTAs cost as much as 3 to 5 tiles.  Measured uncut / cut (us):
-    // 1 row of 2 tiles 10.9 / 12.3, of 4 14.6 / 12.7; 16 rows of 4 14.8 / 13.9, of 8 21.8 / 15.5; 64
-    // rows of 4 15.5 / 19.2, of 8 22.3 / 25.5, of 16 36.1 / 34.5; 300 rows of 4 36.2 / 37.9, of 8
-    // 56.8 / 52.9, of 16 97.5 / 80.5.
+    // In tiles: uncut, the busiest CTA has whole rows to do, one for each time the rows go around
+    // the SMs; cut, all have the same number and, where that is one, the join behind them (2 tiles,
+    // one more for 20 rows); where it is more, most CTAs also change rows inside (5 with the join).
+    // Measured over 1 .. 400 equal rows of 1 .. 8 tiles, uncut / cut (us): 1 row of 2 tiles 11.5 /
+    // 12.5, of 4 14.8 / 12.9; 16 of 4 14.9 / 14.0, of 8 21.8 / 15.0; 28 of 4 15.2 / 15.9, of 7 20.3 /
+    // 22.6; 36 of 6 18.6 / 19.0, of 8 22.3 / 19.3; 40 of 8 22.1 / 23.3; 64 of 4 15.5 / 19.0, of 8 22.4 /
+    // 25.4, of 16 35.9 / 34.3; 149 of 6 32.6 / 30.9 (the rule's worst, 6 %), of 8 40.1 / 35.0; 200 of 8
+    // 41.2 / 47.9; 300 of 4 36.5 / 38.4, of 8 56.6 / 53.0, of 16 98 / 81.
     CachePlan plan;
-    const int64_t idle = (ceil_div(rows, CACHE_MAX_RANGES) * CACHE_MAX_RANGES - rows) * tiles;   // tile slots
+    const int64_t uncut = ceil_div(rows, CACHE_MAX_RANGES) * tiles, cut = ceil_div(rows * tiles, CACHE_MAX_RANGES);
     // long rows are always cut: their true lengths may lie far below max_n
-    plan.whole_rows = tiles <= 8 && idle <= (rows < 32 ? 3 * CACHE_MAX_RANGES : 680);
+    plan.whole_rows = tiles <= 8 && uncut <= cut + (cut == 1 ? 2 + rows / 20 : 5);
     plan.room = static_cast<int>(std::min<int64_t>(CACHE_MAX_RANGES, tiles >= CACHE_MAX_RANGES ? tiles : rows * tiles));
     plan.ranges = plan.whole_rows ? static_cast<int>(std::min<int64_t>(CACHE_MAX_RANGES, rows)) : plan.room;
     return plan;
