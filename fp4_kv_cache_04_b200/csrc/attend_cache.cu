@@ -774,6 +774,9 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         if (moved && lane < HEADS) sm.ref[buf][lane] = -sm.minus_m[rb][lane];
                         if (lane == 0) sm.moved[buf] = moved;
                     }
+                    // P in f16, as the A operand of P V: 2^-11 of each weight, a quarter of the rounding of
+                    // a bf16 output; an fp32 output has 6e-5 (1,501 positions) and less over more.  The
+                    // sums l are of the unrounded weights, in fp32.
                     uint32_t pk[HEADS / 2];
 #pragma unroll
                     for (int h = 0; h < HEADS; h += 2) {
@@ -1120,11 +1123,12 @@ csa2_status launch_attend_cache(const CacheParams& p, const CUtensorMap& codes, 
     csa2_status st = check_launch("attend_cache_kernel");
     if (st != CSA2_OK || p.ranges == 1 || p.whole_rows) return st;
     const int64_t rows = static_cast<int64_t>(p.batch) * p.q_per_seq;
-    // 32 slices of a row up to two blocks an SM, 16 up to the four that are resident at once, else
-    // 8.  32 / 16 slices: 1 row of 131,072 29.3 / 31.3 us, 16 rows of 8,192 34.0 / 33.1.
+    // A row in 32 or 16 slices as long as there are at most two blocks an SM, else in 8.  With 32 / 16 / 8
+    // (us): 1 row of 131,072 29.0 / 31.5 / 34.5, 4 of 32,768 31.2 / 31.8 / 32.5, 9 of 8,192 21.6 / 21.7 /
+    // 21.7, 16 of 8,192 33.2 / 31.8 / 32.0, 37 of 4,096 33.6 / 30.5 / 28.4, 64 of 8,192 76.8 / 71.4 / 69.2.
     const unsigned cut = static_cast<unsigned>(std::min<int64_t>(rows, p.ranges - 1));
     if (cut * 32 <= 2 * CACHE_MAX_RANGES) launch_dependent(join_cache_kernel<32>, dim3(cut, 32), AJ_THREADS, 0, stream, p);
-    else if (cut * 16 <= 4 * CACHE_MAX_RANGES) launch_dependent(join_cache_kernel<16>, dim3(cut, 16), AJ_THREADS, 0, stream, p);
+    else if (cut * 16 <= 2 * CACHE_MAX_RANGES) launch_dependent(join_cache_kernel<16>, dim3(cut, 16), AJ_THREADS, 0, stream, p);
     else launch_dependent(join_cache_kernel<8>, dim3(cut, 8), AJ_THREADS, 0, stream, p);
     return check_launch("join_cache_kernel");
 }
