@@ -278,3 +278,64 @@ def test_selected_attention_right_behind_the_append(csa2):  # noqa: F811
         outs.append(out)
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("window,ratio", [(0, 1), (130, 1), (0, 2), (1, 2)])
+def test_many_queries_of_a_sequence(csa2, window, ratio):  # noqa: F811
+    """A chunk's queries, each from its own position on: more than the row table holds, and a sequence
+    that ends inside the chunk."""
+    run_and_check(csa2, [300, 40, 0], normal(0.3), page=128, window=window, sinks=3 if window else 0, q_per_seq=101, ratio=ratio,
+                  q_pos=[300 * ratio - 101, 0, 5])
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_rows_past_32_bits_of_bytes(csa2, paged):  # noqa: F811
+    """A cache of 17 M rows (4.35 GB of codes): append, read-back and attention at its end."""
+    total, n, B = 17_000_064, 700, 2
+    codes, scales = torch.empty(total, 256, dtype=torch.uint8, device=DEV), torch.empty(total, 32, dtype=torch.uint8, device=DEV)
+    lat = torch.randn(B * n, 512, generator=gen(1), device=DEV).to(BF)
+    seq, pos = torch.arange(B, device=DEV).to(torch.int32).repeat_interleave(n), torch.arange(n, device=DEV).repeat(B)
+    table, offs = None, torch.tensor([total - 2 * n, total - n, total], device=DEV)
+    if paged:
+        last = total // 128 - 1
+        table = torch.tensor([[last, 3, last - 2, last - 7, 0, last - 1], [5, last - 3, last - 5, last - 6, last - 4, 1]],
+                             dtype=torch.int32, device=DEV)
+    csa2.append_rope(csa2.append_args(latent=lat, pos=pos, seq=seq, codes=codes, scales=scales, page_table=table,
+                                      kv_offsets=None if paged else offs, page_rows=128 if paged else 0, norm=False))
+    rows = row_of(seq, pos, offs, table, 128)
+    want = [torch.empty(B * n, k, dtype=torch.uint8, device=DEV) for k in (256, 32)]
+    csa2.quantize_kv(lat, 1, *want)
+    assert torch.equal(codes[rows], want[0]) and torch.equal(scales[rows], want[1])
+    back = torch.empty(B * n, 512, dtype=BF, device=DEV)
+    csa2.dequantize_kv(codes, scales, back, src_row=rows)
+    kv = rows64(*want)
+    assert torch.equal(back.double(), kv)
+    q, out = normal(1.0)(B).to(BF), torch.empty(B, 16, 512, device=DEV)
+    lens = torch.tensor([0, n, 2 * n], device=DEV) if paged else offs
+    attend(csa2, q, out, codes, scales, lens, n, sm_scale=512 ** -0.5, page_table=table, page_rows=128 if paged else 0)
+    for b in range(B):
+        assert check_row(q[b], kv[b * n:(b + 1) * n], 512 ** -0.5, out[b]) <= 1
+
+
+def test_queries_at_strides_past_32_bits(csa2):  # noqa: F811
+    """Tokens 2^31 elements apart: what is read and written there, compared with the same tokens packed."""
+    far = torch.empty((1 << 32) + 256, dtype=BF, device=DEV).as_strided((3, 2, 64), (1 << 31, 128, 1))
+    x = torch.randn(3, 2, 64, generator=gen(5), device=DEV).to(BF)
+    far.copy_(x)
+    kw = dict(pos=torch.tensor([5, 1 << 40, 7], device=DEV), inv_freq=freqs(64))
+    want, out = torch.empty_like(x), torch.empty_like(x)
+    csa2.norm_rope(csa2.rope_args(x=x, out=want, **kw))
+    csa2.norm_rope(csa2.rope_args(x=far, out=out, **kw))
+    assert torch.equal(out, want)
+    csa2.norm_rope(csa2.rope_args(x=far, out=far, **kw))
+    assert torch.equal(far.contiguous(), want)
+
+
+@pytest.mark.parametrize("rows,heads,dim,r", [(7, 16, 512, 64), (301, 3, 72, 30), (2, 1, 8, 8), (33, 2, 1024, 1024)])
+def test_half_split_pairs_in_place(csa2, rows, heads, dim, r):  # noqa: F811
+    x = torch.randn(rows, heads, dim, generator=gen(6), device=DEV).to(BF)
+    out = torch.empty_like(x)
+    kw = dict(pos=torch.arange(rows, device=DEV) * 77, inv_freq=freqs(r), half=True)
+    csa2.norm_rope(csa2.rope_args(x=x, out=out, **kw))
+    csa2.norm_rope(csa2.rope_args(x=x, out=x, **kw))
+    assert torch.equal(x, out)
