@@ -335,6 +335,10 @@ def set_wait_limit(workspace: torch.Tensor, polls: int, stream=None) -> None:
 
 
 # ------------------------------------------------------------------ dense use of the cache
+#
+# rope_args, append_args and cache_args check their tensors and hold them: 6 to 10 us on the host,
+# where a call on a block takes 3.  A loop keeps its blocks, and writes each step's inputs into the
+# tensors that they name.
 
 
 # torch's own calls behind torch.cuda.current_device() and current_stream().cuda_stream, without
@@ -402,7 +406,8 @@ def rope_args(*, x: torch.Tensor, out: torch.Tensor, pos: torch.Tensor | None = 
     """Arguments of norm_rope.  x, out: [rows][heads][dim] (any row and head strides, last
     dimension contiguous; bf16 / f16 / fp32 each); out may be x.  pos int64 [rows] and
     inv_freq fp32 [r/2] rotate the last r channels of each vector (both None: no rotation);
-    weight fp32 [dim] or None with norm.  inverse turns back, half pairs (i, i + r/2)."""
+    weight fp32 [dim] or None with norm.  inverse turns back, half pairs (i, i + r/2).  Keep the
+    block for the calls to come (it costs more than the call)."""
     _need(x.dim() == 3 and out.shape == x.shape, "x and out are [rows][heads][dim] of one shape")
     rows, heads, dim = x.shape
     _need((pos is None) == (inv_freq is None), "pos and inv_freq go together")
@@ -431,7 +436,7 @@ def append_args(*, latent: torch.Tensor, pos: torch.Tensor, codes: torch.Tensor,
     """Arguments of append_rope.  latent [n][512] (bf16 / f16 / fp32, any row stride), pos
     int64 [n] (-1: padding), seq int32 [n] or None (token i belongs to sequence i); the cache
     packed by kv_offsets or paged; idx_proj fp32 [n][64] with idx_k / idx_kscale adds the
-    indexer rows."""
+    indexer rows.  Keep the block for the calls to come."""
     n = latent.shape[0]
     _need(latent.dim() == 2 and latent.shape[1] == D, "latent is [n][512]")
     total = _cache_rows(codes, scales)
@@ -497,7 +502,8 @@ def cache_args(*, batch: int, max_n: int, kv_offsets: torch.Tensor, codes: torch
                workspace: torch.Tensor | None = None) -> CacheArgs:
     """Arguments of attend_cache.  q bf16 and out (bf16 or fp32) [batch * q_per_seq][16][512];
     window 0: every visible position, else the last `window` and the first `sinks` ones; lse
-    fp32 [rows][16] or None; a paged cache as in layer_args."""
+    fp32 [rows][16] or None; a paged cache as in layer_args.  Keep the block (and the
+    workspace) for the calls to come."""
     rows = batch * q_per_seq
     _need(q.dtype == torch.bfloat16 and q.numel() == rows * HEADS * D, "q is bf16 [batch * q_per_seq][16][512]")
     _need(out.numel() == rows * HEADS * D, "out is [batch * q_per_seq][16][512]")

@@ -242,14 +242,18 @@ __device__ __forceinline__ float load1(const typename Elem<T>::type* p) {
 // change by a whole step at a border, so the value they are made of is defined to the bit: the
 // real number rounded to fp32, as the indexer row's values are, and that to bf16 (what a
 // program has that casts its fp32 or fp64 result; off by half a bf16 step and half an fp32
-// step at most).  The sum of squares in 64 bits, 1/sqrt by one 64-bit Newton step from
-// the fp32 one (2^-43); x * w * r in fp32 (off by 3 units at most), and again in 64 bits by
-// the whole warp where one of its 512 results lies within 4 units of a bf16 rounding border
-// (1 token in 14; elsewhere both fp32 values round to the same bf16); the rotated channels in 64 bits throughout, a pair per lane and turn,
-// handed to their group's lane through shared memory.  Bound by instructions and their
-// latencies (900 a token, issue slots half busy; what a token loads is asked for before its
-// norm, which is worth 0.6 us; 64-bit throughout it took 21 us): 8,192 tokens ~10 us, 64 tokens
-// 5.6 us in a graph with their read-back.
+// step at most).  The sum of squares in 64 bits, 1/sqrt by one 64-bit step of Newton-Raphson
+// from the fp32 one (2^-43); x * w * r in fp32 (off by 3 units at most), and again in 64 bits
+// by the whole warp where one of its 512 results lies within 4 units of a bf16 rounding border
+// (1 token in 14; elsewhere both fp32 values round to the same bf16); the rotated channels in
+// 64 bits throughout, a pair per lane and turn, handed to their group's lane through shared
+// memory.
+//
+// Bound by latency: a token is one chain (position, row, sum over 32 lanes, root, sine and
+// cosine, rotation, shared memory, quantisation) of 900 instructions, 8,192 tokens are two
+// waves of blocks, the issue slots are half busy and the 64-bit pipe 7 %.  What a token loads
+// is asked for before its norm, which is worth 0.6 us; 64-bit products throughout took 21 us
+// with the read-back, 14.6 now.  By itself 8,192 tokens 10.9 us, 64 tokens 3.1 (in a graph).
 template <int TI>
 __global__ void __launch_bounds__(32 * AR_WARPS)
 append_rope_kernel(AppendParams p) {

@@ -14,16 +14,17 @@ __device__ __forceinline__ uint32_t e4m3x2_rn(float lo, float hi) {
 }
 
 // nvfp4_group with the hardware's E2M1 rounding (to nearest even, saturating, the sign kept
-// when the magnitude rounds to 0) and a quotient by reciprocal and one residual step: x and s
-// carry at most 8 and 4 significant bits, so x / s is a rounding midpoint of E2M1 exactly or
-// at least 2^-12 away from it.  The residual x - y s is exact in the fma and brings y to
-// within a unit of the quotient, and to the quotient itself where that has 3 bits.
+// when the magnitude rounds to 0) and a quotient by reciprocal and one residual step
+// (Markstein's correction: the residual x - y s is exact in the fma).  x and s carry at most 8
+// and 4 significant bits, so x / s is a rounding midpoint of E2M1 exactly or at least 2^-12
+// away from it; the residual brings y to within a unit of the quotient, and to the quotient
+// itself where that has 3 bits.
 __device__ __forceinline__ uint8_t nvfp4_group_hw(const uint16_t (&h)[16], uint2& codes) {
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = max(top, static_cast<uint32_t>(h[i] & 0x7FFFu));
     if (top >= 0x7F80u) return nvfp4_group(h, codes);      // infinities and NaN as there
-    // amax / 6 by the same two steps: 8 bits over 2, against E4M3's midpoints of 5
+    // amax / 6 by the same correction: 8 bits over 2, against E4M3's midpoints of 5
     const float amax = bf16_bits_to_float(static_cast<uint16_t>(top)), q0 = amax * (1.0f / 6.0f);
     const uint32_t scale_code = e4m3x2_rn(fmaf(fmaf(-q0, 6.0f, amax), 1.0f / 6.0f, q0), 0.0f) & 0xFFu;
     const float s = e4m3_to_float(static_cast<uint8_t>(scale_code));
