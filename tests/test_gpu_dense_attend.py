@@ -339,3 +339,32 @@ def test_half_split_pairs_in_place(csa2, rows, heads, dim, r):  # noqa: F811
     csa2.norm_rope(csa2.rope_args(x=x, out=out, **kw))
     csa2.norm_rope(csa2.rope_args(x=x, out=x, **kw))
     assert torch.equal(x, out)
+
+
+def test_two_graphs_that_share_a_workspace_in_turn(csa2):  # noqa: F811
+    """Captured calls of different batches and plans over one workspace, replayed in turn on one stream."""
+    lens = {"cut": [3000, 1, 777], "uncut": [128] * 70, "window": [5000] * 9}
+    most = csa2.cache_workspace_size(csa2.cache_args(batch=70, max_n=5000, kv_offsets=torch.zeros(71, dtype=torch.int64, device=DEV),
+                                                     codes=torch.empty(1, 256, dtype=torch.uint8, device=DEV),
+                                                     scales=torch.empty(1, 32, dtype=torch.uint8, device=DEV),
+                                                     q=normal(1.0)(70).to(BF), out=normal(1.0)(70)))
+    ws, graphs = csa2.alloc_workspace(most), {}
+    for name, n in lens.items():
+        codes, scales = make_cache(sum(n), 4)
+        q, out = normal(1.0)(len(n)).to(BF), torch.empty(len(n), 16, 512, device=DEV)
+        a = csa2.cache_args(batch=len(n), max_n=max(n), kv_offsets=torch.tensor([0] + n).cumsum(0).to(DEV), codes=codes, scales=scales, q=q,
+                            out=out, sm_scale=512 ** -0.5, window=300 if name == "window" else 0, sinks=4, workspace=ws)
+        csa2.attend_cache(a)
+        torch.cuda.synchronize()
+        alone, g = out.clone(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            csa2.attend_cache(a)
+        graphs[name] = (g, a, out, alone)
+    for _ in range(3):
+        for _, _, out, _ in graphs.values():
+            out.fill_(9.0)
+        for g, _, _, _ in graphs.values():
+            g.replay()
+        torch.cuda.synchronize()
+        assert csa2.check_device_status(ws) == 0
+        assert all(torch.equal(out, alone) for _, _, out, alone in graphs.values())
