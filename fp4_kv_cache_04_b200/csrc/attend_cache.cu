@@ -526,6 +526,7 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
     };
     // Lanes leave a wait one by one: a __syncwarp() stands between it and an instruction that wants
     // the whole warp at once (tensor memory, ldmatrix, barriers).
+
     // every role walks the range's rows by itself: it counts tiles, rw rows
     int it = 0, rw = 0;
     int row = range.row, left = range.count, tile = range.tile;
@@ -774,9 +775,9 @@ attend_cache_kernel(const __grid_constant__ CacheParams p, const __grid_constant
                         if (moved && lane < HEADS) sm.ref[buf][lane] = -sm.minus_m[rb][lane];
                         if (lane == 0) sm.moved[buf] = moved;
                     }
-                    // P in f16, as the A operand of P V: 2^-11 of each weight, a quarter of the rounding of
-                    // a bf16 output; an fp32 output has 6e-5 (1,501 positions) and less over more.  The
-                    // sums l are of the unrounded weights, in fp32.
+                    // P in f16, as the A operand of P V: 2^-11 of each weight, an eighth of a bf16 output's
+                    // own rounding; an fp32 output is off by 6e-5 over 1,501 positions, 2.4e-5 over 65,536.
+                    // The sums l are of the unrounded weights, in fp32.
                     uint32_t pk[HEADS / 2];
 #pragma unroll
                     for (int h = 0; h < HEADS; h += 2) {

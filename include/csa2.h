@@ -552,7 +552,7 @@ typedef struct csa2_cache_args {
                                    calls that may run at the same time                  */
     size_t workspace_bytes;
 } csa2_cache_args;
-/* Bytes of workspace that a call takes; 0 for sizes that it refuses.  Never less for a larger
+/* Bytes of workspace that a call takes; 0 where a size is out of its range.  Never less for a larger
  * batch, q_per_seq, max_n, window (from 1 on; 0, every position, is the largest) or sinks, so
  * a workspace for the largest call serves the smaller ones; at most 9.8 MB. */
 size_t csa2_cache_workspace_size(const csa2_cache_args* a);
